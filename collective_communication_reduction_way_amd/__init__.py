@@ -35,6 +35,13 @@ __all__ = [
     "all_reduce_bucket",
     "all_gather_dim1",
     "reduce_scatter_dim1",
+    "all_reduce_dropout",
+    "reduce_scatter_dropout",
+    "dropout",
+    "all_gather_dropout",
+    "vocab_cross_entropy",
+    "vocab_cross_entropy_grad",
+    "vocab_cross_entropy_workspace_size",
     "all_reduce_hier",
     "hier_workspace_size",
     "cost_ring_all_reduce",
@@ -63,6 +70,11 @@ COLLS = {"all_reduce": 0, "reduce_scatter": 1, "all_gather": 2, "reduce": 3, "br
          "gather": 6}
 MAX_RANKS = 64
 HIER_INTRA_RING, HIER_WIRE_ROUND, HIER_STAGED = 1, 2, 4
+
+
+class _Dropout(ctypes.Structure):
+    _fields_ = [("drop", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("offset_dev", ctypes.c_void_p)]
 
 
 class _Link(ctypes.Structure):
@@ -114,6 +126,13 @@ def lib():
         "rr_all_reduce_bucket": (I, [PP, PP, ctypes.POINTER(ctypes.c_size_t), I, I, I, I, P]),
         "rr_all_gather_dim1": (I, [PP, PP, I, S, S, I, P]),
         "rr_reduce_scatter_dim1": (I, [PP, PP, I, S, S, I, I, P]),
+        "rr_all_reduce_dropout": (I, [PP, PP, PP, I, S, I, _Dropout, P]),
+        "rr_reduce_scatter_dropout": (I, [PP, PP, PP, I, S, I, _Dropout, P]),
+        "rr_dropout": (I, [PP, PP, PP, I, S, I, _Dropout, P]),
+        "rr_all_gather_dropout": (I, [PP, PP, I, S, I, _Dropout, P]),
+        "rr_vocab_cross_entropy": (I, [P, PP, P, I, P, P, I, S, S, S, I, P, S, P]),
+        "rr_vocab_cross_entropy_grad": (I, [P, PP, P, I, P, P, P, PP, I, S, S, S, I, P, S, P]),
+        "rr_vocab_cross_entropy_workspace_size": (S, [I, S, S, S, I, I]),
         "rr_all_reduce_hier": (I, [PP, PP, I, S, I, I, I, I, P, S, P]),
         "rr_hier_workspace_size": (S, [I, I, S, I, I]),
         "rr_cost_ring_all_reduce": (I, [I, ctypes.c_double, _Link, ctypes.POINTER(ctypes.c_double)]),
@@ -248,6 +267,19 @@ def _call_workspace(nbytes, t, stream):
             stream = torch.cuda.ExternalStream(stream, device=t.device)
         ws.record_stream(stream)
     return ws
+
+
+def _call_output(t, shape, dtype, stream):
+    """An output tensor for one call, allocated on the current stream and marked
+    as used by the stream the kernels go to (as _call_workspace)."""
+    import torch
+
+    out = torch.empty(shape, dtype=dtype, device=t.device)
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        out.record_stream(stream)
+    return out
 
 
 def _op(op):
@@ -450,6 +482,231 @@ def reduce_scatter_dim1(ins, outs, op="sum", stream=None):
                                   p, rows, cols, _dtype_code(ins[0]), _op(op), _stream(ins[0], stream))
     _check(st, "rr_reduce_scatter_dim1")
     return outs
+
+
+def _drop(drop, seed, offset, offset_dev, device):
+    import torch
+
+    ptr = None
+    if offset_dev is not None:
+        if offset_dev.dtype != torch.int64 or offset_dev.numel() != 1 or offset_dev.device != device:
+            raise ValueError("offset_dev must be one int64 on the buffers' device")
+        ptr = offset_dev.data_ptr()
+    mask = (1 << 64) - 1
+    return _Dropout(float(drop), int(seed) & mask, int(offset) & mask, ptr)
+
+
+def _residuals(residuals, outs, what):
+    """The residual pointers (or None): a list of p tensors, or a 2-D tensor."""
+    if residuals is None:
+        return None
+    res = _ranks(residuals, f"{what} residuals")
+    if len(res) != len(outs) or any(a.numel() != o.numel() for a, o in zip(res, outs)) or (
+            res[0].dtype != outs[0].dtype or res[0].device != outs[0].device):
+        raise ValueError(f"{what}: residuals must match the outputs in count, length, dtype and device")
+    return _ptr_array([t.data_ptr() for t in res])
+
+
+def _same_place(a, b, what):
+    if a.dtype != b.dtype or a.device != b.device:
+        raise ValueError(f"{what}: inputs and outputs must share device and dtype")
+
+
+def all_reduce_dropout(ins, outs=None, drop=0.1, seed=0, offset=0, residuals=None, offset_dev=None, stream=None):
+    """Every rank's output becomes its residual plus the dropped-out sum of the
+    p inputs (outs=None: in place).
+
+    The mask depends on (seed, offset) and the element's index alone, and is
+    never stored; ``offset_dev``, an int64 tensor of one element, is added to
+    ``offset`` when the kernel runs (for captured graphs).  ``residuals``: None,
+    or one tensor per rank (the same tensor may stand for several).  Gradient
+    of the inputs: ``dropout`` of each rank's output gradient with the same
+    (seed, offset), where the ranks hold copies of one loss.
+    """
+    ins = _ranks(ins, "all_reduce_dropout inputs")
+    outs = ins if outs is None else _ranks(outs, "all_reduce_dropout outputs")
+    p, n = len(ins), ins[0].numel()
+    _same_place(ins[0], outs[0], "all_reduce_dropout")
+    if len(outs) != p or any(t.numel() != n for t in ins + outs):
+        raise ValueError("all_reduce_dropout: need p inputs and p outputs of equal length")
+    res = _residuals(residuals, outs, "all_reduce_dropout")
+    st = lib().rr_all_reduce_dropout(_ptr_array([t.data_ptr() for t in ins]), res,
+                                     _ptr_array([t.data_ptr() for t in outs]), p, n, _dtype_code(ins[0]),
+                                     _drop(drop, seed, offset, offset_dev, ins[0].device), _stream(ins[0], stream))
+    _check(st, "rr_all_reduce_dropout")
+    return outs
+
+
+def reduce_scatter_dropout(ins, outs, drop=0.1, seed=0, offset=0, residuals=None, offset_dev=None, stream=None):
+    """Rank c's output (n/p elements) becomes its residual plus chunk c of the
+    dropped-out sum.  Gradient of the inputs: ``all_gather_dropout``."""
+    ins = _ranks(ins, "reduce_scatter_dropout inputs")
+    outs = _ranks(outs, "reduce_scatter_dropout outputs")
+    p, n = len(ins), ins[0].numel()
+    _same_place(ins[0], outs[0], "reduce_scatter_dropout")
+    if len(outs) != p or any(t.numel() != n for t in ins) or any(o.numel() * p != n for o in outs):
+        raise ValueError("reduce_scatter_dropout: need p inputs of n and p outputs of n/p elements")
+    res = _residuals(residuals, outs, "reduce_scatter_dropout")
+    st = lib().rr_reduce_scatter_dropout(_ptr_array([t.data_ptr() for t in ins]), res,
+                                         _ptr_array([t.data_ptr() for t in outs]), p, n, _dtype_code(ins[0]),
+                                         _drop(drop, seed, offset, offset_dev, ins[0].device),
+                                         _stream(ins[0], stream))
+    _check(st, "rr_reduce_scatter_dropout")
+    return outs
+
+
+def dropout(ins, outs=None, drop=0.1, seed=0, offset=0, residuals=None, offset_dev=None, stream=None):
+    """Every rank's output becomes its residual plus its own dropped-out input
+    (outs=None: in place), one mask for all ranks."""
+    ins = _ranks(ins, "dropout inputs")
+    outs = ins if outs is None else _ranks(outs, "dropout outputs")
+    p, n = len(ins), ins[0].numel()
+    _same_place(ins[0], outs[0], "dropout")
+    if len(outs) != p or any(t.numel() != n for t in ins + outs):
+        raise ValueError("dropout: need p inputs and p outputs of equal length")
+    res = _residuals(residuals, outs, "dropout")
+    st = lib().rr_dropout(_ptr_array([t.data_ptr() for t in ins]), res, _ptr_array([t.data_ptr() for t in outs]), p,
+                          n, _dtype_code(ins[0]), _drop(drop, seed, offset, offset_dev, ins[0].device),
+                          _stream(ins[0], stream))
+    _check(st, "rr_dropout")
+    return outs
+
+
+def all_gather_dropout(ins, outs, drop=0.1, seed=0, offset=0, offset_dev=None, stream=None):
+    """Every rank's output (n elements) becomes the dropped-out concatenation of
+    the p shards."""
+    ins = _ranks(ins, "all_gather_dropout inputs")
+    outs = _ranks(outs, "all_gather_dropout outputs")
+    p, n = len(ins), outs[0].numel()
+    _same_place(ins[0], outs[0], "all_gather_dropout")
+    if len(outs) != p or any(o.numel() != n for o in outs) or any(i.numel() * p != n for i in ins):
+        raise ValueError("all_gather_dropout: need p shards of n/p elements and p outputs of n")
+    st = lib().rr_all_gather_dropout(_ptr_array([t.data_ptr() for t in ins]),
+                                     _ptr_array([t.data_ptr() for t in outs]), p, n, _dtype_code(ins[0]),
+                                     _drop(drop, seed, offset, offset_dev, ins[0].device), _stream(ins[0], stream))
+    _check(st, "rr_all_gather_dropout")
+    return outs
+
+
+def vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, dtype, grad=False):
+    """Bytes of workspace vocab_cross_entropy (or its gradient) needs."""
+    import torch
+
+    if isinstance(dtype, torch.dtype):
+        dtype = _dtype_name(dtype)
+    return int(lib().rr_vocab_cross_entropy_workspace_size(int(p), int(tokens), int(dim), int(vocab), DTYPES[dtype],
+                                                           1 if grad else 0))
+
+
+def _vocab_shards(weights, hidden, what):
+    """The p shards [V_r, dim], V_r = the chunk lengths of their sum."""
+    import torch
+
+    weights = list(weights.unbind(0)) if isinstance(weights, torch.Tensor) and weights.dim() == 3 else list(weights)
+    if not weights:
+        raise ValueError(f"{what}: no weight shards")
+    dim = hidden.shape[1]
+    for w in weights:
+        if w.dim() != 2 or w.shape[1] != dim or not w.is_contiguous():
+            raise ValueError(f"{what}: weight shards must be contiguous [V_r, {dim}] matrices")
+        if w.dtype != hidden.dtype or w.device != hidden.device:
+            raise ValueError(f"{what}: weight shards and hidden states must share device and dtype")
+    p, vocab = len(weights), sum(w.shape[0] for w in weights)
+    if any(w.shape[0] != (r + 1) * vocab // p - r * vocab // p for r, w in enumerate(weights)):
+        raise ValueError(f"{what}: shard r must hold the rows floor(r V / p) .. floor((r + 1) V / p) of V = {vocab}")
+    return weights, p, vocab
+
+
+def _vocab_args(hidden, weights, targets, what):
+    import torch
+
+    if hidden.dim() != 2 or not hidden.is_contiguous():
+        raise ValueError(f"{what}: hidden states must be a contiguous [tokens, dim] matrix")
+    weights, p, vocab = _vocab_shards(weights, hidden, what)
+    if targets.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{what}: targets must be int32 or int64")
+    if targets.shape != (hidden.shape[0],) or not targets.is_contiguous() or targets.device != hidden.device:
+        raise ValueError(f"{what}: need one contiguous target per token on the hidden states' device")
+    return weights, p, vocab
+
+
+def _per_token(t, hidden, what, name):
+    import torch
+
+    if t.dtype != torch.float32 or t.shape != (hidden.shape[0],) or not t.is_contiguous() or t.device != hidden.device:
+        raise ValueError(f"{what}: {name} must be a contiguous float32 value per token on the hidden states' device")
+
+
+def vocab_cross_entropy(hidden, weights, targets, loss=None, lse=None, workspace=None, stream=None):
+    """Softmax cross entropy of hidden states [tokens, dim] against a vocabulary
+    cut over p ranks (``weights``: p shards [V_r, dim]); returns (loss, lse),
+    float32, one value per token.  The logits are never kept.  A target
+    outside the vocabulary masks its token (loss 0).  ``loss``, ``lse`` and the
+    workspace are allocated with torch when not given.
+    """
+    import torch
+
+    what = "vocab_cross_entropy"
+    weights, p, vocab = _vocab_args(hidden, weights, targets, what)
+    tokens, dim = hidden.shape
+    handle = _stream(hidden, stream)
+    loss, lse = (_call_output(hidden, (tokens,), torch.float32, stream) if t is None else t for t in (loss, lse))
+    _per_token(loss, hidden, what, "loss")
+    _per_token(lse, hidden, what, "lse")
+    code = _dtype_code(hidden)
+    need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 0))
+    if workspace is None:
+        workspace = _call_workspace(need, hidden, stream)
+    st = lib().rr_vocab_cross_entropy(hidden.data_ptr(), _ptr_array([w.data_ptr() for w in weights]),
+                                      targets.data_ptr(), targets.element_size(), loss.data_ptr(), lse.data_ptr(), p,
+                                      tokens, dim, vocab, code, workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), handle)
+    _check(st, "rr_vocab_cross_entropy")
+    return loss, lse
+
+
+def vocab_cross_entropy_grad(hidden, weights, targets, lse, grad_loss, dhidden=None, dweights=None, workspace=None,
+                             stream=None, need_hidden=True, need_weights=True):
+    """Gradients of ``vocab_cross_entropy`` for the losses' gradients
+    ``grad_loss`` (float32, one per token); returns (dhidden, dweights) shaped
+    and typed as hidden and weights.  ``lse``: what vocab_cross_entropy
+    returned for the same inputs.  A side that is not needed is not computed
+    and returned as None.
+    """
+    what = "vocab_cross_entropy_grad"
+    weights, p, vocab = _vocab_args(hidden, weights, targets, what)
+    tokens, dim = hidden.shape
+    handle = _stream(hidden, stream)
+    _per_token(lse, hidden, what, "lse")
+    _per_token(grad_loss, hidden, what, "grad_loss")
+    if need_hidden:
+        if dhidden is None:
+            dhidden = _call_output(hidden, hidden.shape, hidden.dtype, stream)
+        if dhidden.shape != hidden.shape or dhidden.dtype != hidden.dtype or not dhidden.is_contiguous() or (
+                dhidden.device != hidden.device):
+            raise ValueError(f"{what}: dhidden must match the hidden states")
+    else:
+        dhidden = None
+    if need_weights:
+        if dweights is None:
+            dweights = [_call_output(hidden, w.shape, w.dtype, stream) for w in weights]
+        dweights = list(dweights)
+        if len(dweights) != p or any(g.shape != w.shape or g.dtype != w.dtype or not g.is_contiguous() or
+                                     g.device != w.device for g, w in zip(dweights, weights)):
+            raise ValueError(f"{what}: dweights must match the weight shards")
+    else:
+        dweights = None
+    code = _dtype_code(hidden)
+    need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 1))
+    if workspace is None:
+        workspace = _call_workspace(need, hidden, stream)
+    st = lib().rr_vocab_cross_entropy_grad(
+        hidden.data_ptr(), _ptr_array([w.data_ptr() for w in weights]), targets.data_ptr(), targets.element_size(),
+        lse.data_ptr(), grad_loss.data_ptr(), None if dhidden is None else dhidden.data_ptr(),
+        None if dweights is None else _ptr_array([g.data_ptr() for g in dweights]), p, tokens, dim, vocab, code,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    _check(st, "rr_vocab_cross_entropy_grad")
+    return dhidden, dweights
 
 
 def _hier_flags(intra, wire_round, staged):

@@ -33,6 +33,12 @@ SOURCES = [
     "rr_multi.hip",
     "rr_exec.hip",
     "rr_scratch.hip",
+    "rr_dropout.hip",
+    "rr_vocab_f32.hip",
+    "rr_vocab_bf16.hip",
+    "rr_vocab_f16.hip",
+    "rr_vocab_aux.hip",
+    "rr_vocab.cpp",
     "rr_phase_ring.hip",
     "rr_phase_hier.hip",
     "rr_phase_hier_var.hip",

@@ -25,6 +25,7 @@
 #include "rr.h"
 #include "rr_kernels.h"
 #include "rr_plan.h"
+#include "rr_vocab.h"
 
 namespace {
 
@@ -1200,6 +1201,463 @@ rr_status_t rr_reduce_scatter_dim1(const void* const* sendbufs, void* const* rec
   const hipError_t e = rr::launch_fold_cols(a, kind_of(dtype), op, vec ? 1 : 0, t.multi_per_cu,
                                             reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "reduce_scatter_dim1");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+// Dropout on the way through the collectives.
+
+static rr_status_t check_float_dtype(rr_dtype_t dt, const char* what) {
+  rr_status_t st = check_dtype(dt);
+  if (st) return st;
+  if (dt == RR_INT32) return fail(RR_ERROR_UNSUPPORTED, "%s is defined for float dtypes only", what);
+  return RR_SUCCESS;
+}
+
+// Fills the generator's fields; drop in [0, 1) (the comparison also refuses NaN).
+static rr_status_t drop_params(rr::DropArgs& a, const rr_dropout_t& d) {
+  if (!(d.drop >= 0.0 && d.drop < 1.0))
+    return fail(RR_ERROR_INVALID_ARGUMENT, "drop=%g outside [0, 1)", d.drop);
+  if (reinterpret_cast<uintptr_t>(d.offset_dev) % 8)
+    return fail(RR_ERROR_INVALID_ARGUMENT, "offset_dev is not aligned to 8 bytes");
+  a.seed = d.seed;
+  a.offset = d.offset;
+  a.offset_dev = d.offset_dev;
+  a.threshold = static_cast<uint32_t>(d.drop * 4294967296.0);
+  a.scale = static_cast<float>(1.0 / (1.0 - d.drop));
+  return RR_SUCCESS;
+}
+
+// The four forms: in_len / out_len elements per input / output (and residual) buffer.
+static rr_status_t run_dropout(const char* what, rr::DropForm form, const void* const* send, const void* const* residuals,
+                        void* const* recv, int p, size_t n, uint64_t in_len, uint64_t out_len, rr_dtype_t dtype,
+                        const rr_dropout_t& drop, rr_stream_t stream) {
+  rr::DropArgs a;
+  memset(&a, 0, sizeof(a));
+  rr_status_t st = drop_params(a, drop);
+  if (st) return st;
+  const size_t esz = rr::elem_size(dtype);
+  if ((st = check_rank_arrays(send, recv, p, esz, n))) return st;
+  if (n == 0) return ok();
+  const bool shard_in = form == rr::DropForm::kGather, shard_out = form == rr::DropForm::kScatter;
+  std::vector<Range> outs, ins;
+  bool vec = true, one = true;
+  for (int r = 0; r < p; ++r) {
+    a.in[r] = send[r];
+    a.out[r] = recv[r];
+    vec = vec && aligned16(send[r]) && aligned16(recv[r]);
+    outs.push_back(range_of(recv[r], out_len * esz, r));
+    ins.push_back(range_of(send[r], in_len * esz, r));
+    if (!residuals) continue;
+    if ((st = check_buf(residuals[r], esz, "residuals", r))) return st;
+    a.res[r] = residuals[r];
+    vec = vec && aligned16(residuals[r]);
+    one = one && residuals[r] == residuals[0];
+  }
+  // In place: a rank's output may be its own input (the chunk's slot on a
+  // sharded side) ...
+  st = check_aliasing(outs, ins, [&](const Range& o, const Range& i) {
+    if (o.rank != i.rank) return false;
+    if (shard_in) return i.lo == o.lo + static_cast<uint64_t>(o.rank) * in_len * esz;
+    if (shard_out) return o.lo == i.lo + static_cast<uint64_t>(o.rank) * out_len * esz;
+    return o.lo == i.lo;
+  });
+  if (st) return st;
+  if (residuals) {
+    // ... or its own residual; an output over a residual that other ranks
+    // read as well would overwrite it under them.
+    std::vector<Range> res;
+    for (int r = 0; r < p; ++r) res.push_back(range_of(residuals[r], out_len * esz, r));
+    st = check_aliasing(outs, res, [](const Range& o, const Range& i) { return o.rank == i.rank && o.lo == i.lo; });
+    if (st) return st;
+  }
+  a.has_res = residuals ? 1 : 0;
+  a.one_res = one && p > 1 ? 1 : 0;
+  a.p = p;
+  if (form == rr::DropForm::kRanks) {
+    a.chunks = 1;
+    a.bound[1] = n;
+  } else {
+    a.chunks = p;
+    rr::chunk_bounds(p, n, a.bound);
+  }
+  // a sharded side's groups must start on its 16-byte boundaries
+  if ((shard_in || shard_out) && ((n / p) * esz) % 16) vec = false;
+  a.vec = vec ? 1 : 0;
+  const Tuning& t = tuning();
+  if (t.log)
+    fprintf(stderr, "[rr] %s: p=%d n=%zu vec=%d residuals=%d\n", what, p, n, a.vec, a.has_res ? (a.one_res ? 1 : p) : 0);
+  const hipError_t e = rr::launch_dropout(a, form, kind_of(dtype), reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, what);
+  return ok();
+}
+
+static rr_status_t check_shards(int p, size_t n) {
+  if (n % static_cast<size_t>(p))
+    return fail(RR_ERROR_INVALID_ARGUMENT, "n=%zu is not divisible by p=%d", n, p);
+  return RR_SUCCESS;
+}
+
+rr_status_t rr_all_reduce_dropout(const void* const* sendbufs, const void* const* residuals, void* const* recvbufs,
+                                  int p, size_t n, rr_dtype_t dtype, rr_dropout_t drop, rr_stream_t stream) {
+  rr_status_t st;
+  if ((st = check_p(p)) || (st = check_float_dtype(dtype, "dropout")) || (st = check_n(n))) return st;
+  return run_dropout("all_reduce_dropout", rr::DropForm::kReduce, sendbufs, residuals, recvbufs, p, n, n, n, dtype,
+                     drop, stream);
+}
+
+rr_status_t rr_reduce_scatter_dropout(const void* const* sendbufs, const void* const* residuals,
+                                      void* const* recvbufs, int p, size_t n, rr_dtype_t dtype, rr_dropout_t drop,
+                                      rr_stream_t stream) {
+  rr_status_t st;
+  if ((st = check_p(p)) || (st = check_float_dtype(dtype, "dropout")) || (st = check_n(n)) || (st = check_shards(p, n)))
+    return st;
+  return run_dropout("reduce_scatter_dropout", rr::DropForm::kScatter, sendbufs, residuals, recvbufs, p, n, n, n / p,
+                     dtype, drop, stream);
+}
+
+rr_status_t rr_dropout(const void* const* sendbufs, const void* const* residuals, void* const* recvbufs, int p,
+                       size_t n, rr_dtype_t dtype, rr_dropout_t drop, rr_stream_t stream) {
+  rr_status_t st;
+  if ((st = check_p(p)) || (st = check_float_dtype(dtype, "dropout")) || (st = check_n(n))) return st;
+  return run_dropout("dropout", rr::DropForm::kRanks, sendbufs, residuals, recvbufs, p, n, n, n, dtype, drop, stream);
+}
+
+rr_status_t rr_all_gather_dropout(const void* const* sendbufs, void* const* recvbufs, int p, size_t n,
+                                  rr_dtype_t dtype, rr_dropout_t drop, rr_stream_t stream) {
+  rr_status_t st;
+  if ((st = check_p(p)) || (st = check_float_dtype(dtype, "dropout")) || (st = check_n(n)) || (st = check_shards(p, n)))
+    return st;
+  return run_dropout("all_gather_dropout", rr::DropForm::kGather, sendbufs, nullptr, recvbufs, p, n, n / p, n, dtype,
+                     drop, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Vocabulary-parallel softmax cross entropy.
+
+constexpr uint64_t kMaxRows = 1ull << 23;   // tokens, vocabulary: 32-bit grids and columns
+constexpr uint64_t kMaxDim = 1ull << 20;
+constexpr uint64_t kMaxMatrix = 1ull << 36; // elements of the hidden states and of the output weight
+
+static rr_status_t check_vocab_shape(int p, size_t tokens, size_t dim, size_t vocab, rr_dtype_t dtype) {
+  rr_status_t st;
+  if ((st = check_p(p)) || (st = check_float_dtype(dtype, "the vocabulary cross entropy"))) return st;
+  if (dim < 1 || dim > kMaxDim) return fail(RR_ERROR_INVALID_ARGUMENT, "dim=%zu outside [1, 2^20]", dim);
+  if (vocab < 1 || vocab > kMaxRows) return fail(RR_ERROR_INVALID_ARGUMENT, "vocab=%zu outside [1, 2^23]", vocab);
+  if (tokens > kMaxRows) return fail(RR_ERROR_INVALID_ARGUMENT, "tokens=%zu exceeds 2^23", tokens);
+  if (static_cast<uint64_t>(tokens) * dim > kMaxMatrix || static_cast<uint64_t>(vocab) * dim > kMaxMatrix)
+    return fail(RR_ERROR_INVALID_ARGUMENT, "tokens*dim or vocab*dim exceeds 2^36");
+  return RR_SUCCESS;
+}
+
+// What both directions read, and the workspace.  Adds the ranges of the inputs.
+static rr_status_t check_vocab_inputs(const void* hidden, const void* const* weights, const void* targets, int target_bytes,
+                               int p, size_t tokens, size_t dim, size_t vocab, rr_dtype_t dtype, bool grad,
+                               void* workspace, size_t workspace_bytes, std::vector<Range>& ins, bool& pack) {
+  const size_t esz = rr::elem_size(dtype);
+  rr_status_t st;
+  if (target_bytes != 4 && target_bytes != 8)
+    return fail(RR_ERROR_INVALID_ARGUMENT, "target_bytes=%d (use 4 or 8)", target_bytes);
+  if (!weights) return fail(RR_ERROR_INVALID_ARGUMENT, "weights is NULL");
+  pack = (dim * esz) % 16 != 0;
+  if (tokens > 0) {
+    if ((st = check_buf(hidden, esz, "hidden", 0)) || (st = check_buf(targets, target_bytes, "targets", 0))) return st;
+    ins.push_back(range_of(hidden, tokens * dim * esz, -1));
+    ins.push_back(range_of(targets, tokens * target_bytes, -2));
+    pack = pack || !aligned16(hidden);
+  }
+  uint64_t b[RR_MAX_RANKS + 1];
+  rr::chunk_bounds(p, vocab, b);
+  for (int r = 0; r < p; ++r) {
+    if (b[r + 1] == b[r]) continue;
+    if ((st = check_buf(weights[r], esz, "weights", r))) return st;
+    ins.push_back(range_of(weights[r], (b[r + 1] - b[r]) * dim * esz, r));
+    pack = pack || !aligned16(weights[r]);
+  }
+  const size_t need = rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, dtype, grad ? 1 : 0);
+  if (need > 0) {
+    if (!workspace) return fail(RR_ERROR_INVALID_ARGUMENT, "workspace is NULL (%zu bytes needed)", need);
+    if (!aligned16(workspace)) return fail(RR_ERROR_INVALID_ARGUMENT, "workspace is not 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(RR_ERROR_INVALID_ARGUMENT, "workspace of %zu bytes is smaller than the %zu needed", workspace_bytes,
+                  need);
+  }
+  return RR_SUCCESS;
+}
+
+size_t rr_vocab_cross_entropy_workspace_size(int p, size_t tokens, size_t dim, size_t vocab, rr_dtype_t dtype,
+                                             int grad) {
+  if (check_vocab_shape(p, tokens, dim, vocab, dtype)) return 0;
+  ok();
+  rr::VocabPlan aligned, packed;
+  rr::plan_vocab(packed, p, tokens, dim, vocab, dtype, grad != 0, true);
+  if ((dim * rr::elem_size(dtype)) % 16) return packed.total;
+  rr::plan_vocab(aligned, p, tokens, dim, vocab, dtype, grad != 0, false);
+  return std::max(aligned.total, packed.total);
+}
+
+// The piece's columns and, when the inputs are copied first, its weight rows:
+// sh.w[r] then points where row 0 of shard r would lie (only rows of the piece
+// are read).
+static hipError_t vocab_piece(const rr::VocabPlan& pl, const rr::VocabShards& sh, bool pack, Kind k, uint32_t c0, uint32_t c1,
+                       char* ws, rr::VocabShards& out, hipStream_t s) {
+  out = sh;
+  if (!pack) return hipSuccess;
+  const uint64_t row = static_cast<uint64_t>(pl.dim_pad) * pl.esz;
+  rr::PackWeightArgs a;
+  a.sh = sh;
+  a.out = ws + pl.pack_w;
+  a.out_stride = row;
+  a.dim = pl.dim;
+  a.c0 = c0;
+  a.c1 = c1;
+  const hipError_t e = rr::launch_pack_weight(a, k, s);
+  for (int r = 0; r < sh.p; ++r) {
+    const uintptr_t base = reinterpret_cast<uintptr_t>(ws + pl.pack_w);
+    out.w[r] = reinterpret_cast<const void*>(base + static_cast<uint64_t>(sh.off[r]) * row - static_cast<uint64_t>(c0) * row);
+  }
+  return e;
+}
+
+static uint32_t tiles_over(uint64_t n, uint32_t t) { return static_cast<uint32_t>((n + t - 1) / t); }
+
+rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weights, const void* targets,
+                                   int target_bytes, float* loss, float* lse, int p, size_t tokens, size_t dim,
+                                   size_t vocab, rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                   rr_stream_t stream) {
+  rr_status_t st;
+  std::vector<Range> ins, outs;
+  bool pack = false;
+  if ((st = check_vocab_shape(p, tokens, dim, vocab, dtype)) ||
+      (st = check_vocab_inputs(hidden, weights, targets, target_bytes, p, tokens, dim, vocab, dtype, false, workspace,
+                               workspace_bytes, ins, pack)))
+    return st;
+  if (tokens == 0) return ok();
+  if ((st = check_buf(loss, 4, "loss", 0)) || (st = check_buf(lse, 4, "lse", 0))) return st;
+  outs.push_back(range_of(loss, tokens * 4, -3));
+  outs.push_back(range_of(lse, tokens * 4, -4));
+  outs.push_back(range_of(workspace, workspace_bytes, -5));
+  if ((st = check_aliasing(outs, ins, [](const Range&, const Range&) { return false; }))) return st;
+
+  rr::VocabPlan pl;
+  rr::plan_vocab(pl, p, tokens, dim, vocab, dtype, false, pack);
+  const Kind k = kind_of(dtype);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const Tuning& t = tuning();
+  if (t.log)
+    fprintf(stderr, "[rr] vocab_cross_entropy: p=%d tokens=%zu dim=%zu vocab=%zu pieces=%u tile=%d copy=%d\n", p, tokens,
+            dim, vocab, pl.pieces, static_cast<int>(pl.logits_tile), pack ? 1 : 0);
+  rr::VocabShards sh = pl.sh;
+  for (int r = 0; r < p; ++r) sh.w[r] = weights[r];
+  hipError_t e = hipSuccess;
+  rr::LogitArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = hidden;
+  a.x_stride = dim * pl.esz;
+  a.w_stride = a.x_stride;
+  a.kbytes = static_cast<uint32_t>(a.x_stride);
+  if (pack) {
+    rr::PackRowsArgs c;
+    memset(&c, 0, sizeof(c));
+    c.x = hidden;
+    c.out = ws + pl.pack_x;
+    c.out_stride = static_cast<uint64_t>(pl.dim_pad) * pl.esz;
+    c.tokens = c.rows = pl.tokens;
+    c.dim = pl.dim;
+    c.vocab = pl.sh.vocab;
+    if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy: copy");
+    a.x = c.out;
+    a.x_stride = a.w_stride = c.out_stride;
+    a.kbytes = static_cast<uint32_t>(c.out_stride);
+  }
+  a.targets = targets;
+  a.target_bytes = target_bytes;
+  a.part = reinterpret_cast<float*>(ws + pl.part);
+  a.hit = reinterpret_cast<float*>(ws + pl.hit);
+  a.tokens = pl.tokens;
+  a.tiles_n = tiles_over(tokens, rr::tile_n(pl.logits_tile));
+  for (uint32_t c0 = 0; c0 < pl.sh.off[p]; c0 += pl.piece) {
+    a.c0 = c0;
+    a.c1 = std::min(pl.sh.off[p], c0 + pl.piece);
+    if ((e = vocab_piece(pl, sh, pack, k, a.c0, a.c1, ws, a.sh, s)) != hipSuccess)
+      return hip_fail(e, "vocab_cross_entropy: copy");
+    a.tiles_m = tiles_over(a.c1 - a.c0, rr::tile_m(pl.logits_tile));
+    if ((e = rr::launch_logits(a, k, pl.logits_tile, false, s)) != hipSuccess)
+      return hip_fail(e, "vocab_cross_entropy: logits");
+    a.tile0 += a.tiles_m;
+  }
+  rr::LossArgs l;
+  l.part = a.part;
+  l.hit = a.hit;
+  l.targets = targets;
+  l.target_bytes = target_bytes;
+  l.loss = loss;
+  l.lse = lse;
+  l.tokens = pl.tokens;
+  l.tiles = a.tile0;
+  l.vocab = pl.sh.vocab;
+  if ((e = rr::launch_loss(l, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy: loss");
+  return ok();
+}
+
+rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* weights, const void* targets,
+                                        int target_bytes, const float* lse, const float* grad_loss, void* dhidden,
+                                        void* const* dweights, int p, size_t tokens, size_t dim, size_t vocab,
+                                        rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                        rr_stream_t stream) {
+  rr_status_t st;
+  std::vector<Range> ins, outs;
+  bool pack = false;
+  if ((st = check_vocab_shape(p, tokens, dim, vocab, dtype)) ||
+      (st = check_vocab_inputs(hidden, weights, targets, target_bytes, p, tokens, dim, vocab, dtype, true, workspace,
+                               workspace_bytes, ins, pack)))
+    return st;
+  if (!dhidden && !dweights) return fail(RR_ERROR_INVALID_ARGUMENT, "dhidden and dweights are both NULL");
+  const size_t esz = rr::elem_size(dtype);
+  if (tokens > 0) {
+    if ((st = check_buf(lse, 4, "lse", 0)) || (st = check_buf(grad_loss, 4, "grad_loss", 0))) return st;
+    ins.push_back(range_of(lse, tokens * 4, -3));
+    ins.push_back(range_of(grad_loss, tokens * 4, -4));
+    if (dhidden) {
+      if ((st = check_buf(dhidden, esz, "dhidden", 0))) return st;
+      outs.push_back(range_of(dhidden, tokens * dim * esz, -5));
+    }
+  }
+  rr::VocabPlan pl;
+  rr::plan_vocab(pl, p, tokens, dim, vocab, dtype, true, pack);
+  if (dweights) {
+    for (int r = 0; r < p; ++r) {
+      if (pl.sh.rows[r] == 0) continue;
+      if ((st = check_buf(dweights[r], esz, "dweights", r))) return st;
+      outs.push_back(range_of(dweights[r], static_cast<uint64_t>(pl.sh.rows[r]) * dim * esz, r));
+    }
+  }
+  outs.push_back(range_of(workspace, workspace_bytes, -6));
+  if ((st = check_aliasing(outs, ins, [](const Range&, const Range&) { return false; }))) return st;
+  if (tokens == 0 && !dweights) return ok();
+
+  const Kind k = kind_of(dtype);
+  const bool f16 = dtype == RR_FLOAT16;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const uint64_t row = static_cast<uint64_t>(pl.dim_pad) * pl.esz;
+  const Tuning& t = tuning();
+  if (t.log)
+    fprintf(stderr,
+            "[rr] vocab_cross_entropy_grad: p=%d tokens=%zu dim=%zu vocab=%zu pieces=%u tiles=%d/%d/%d splits=%u copy=%d\n",
+            p, tokens, dim, vocab, pl.pieces, static_cast<int>(pl.logits_tile), static_cast<int>(pl.hidden_tile),
+            static_cast<int>(pl.weight_tile), pl.splits, pack ? 1 : 0);
+  rr::VocabShards sh = pl.sh;
+  for (int r = 0; r < p; ++r) sh.w[r] = weights[r];
+  hipError_t e = hipSuccess;
+  float* scale = reinterpret_cast<float*>(ws + pl.scale);
+  if (f16) {
+    e = rr::launch_grad_scale(grad_loss, targets, target_bytes, pl.tokens, pl.sh.vocab, scale, s);
+    if (e != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: scale");
+  }
+  // The hidden rows that count, the others zero: a masked token's row may
+  // hold anything, and 0 * NaN must not reach dweights.
+  rr::PackRowsArgs c;
+  memset(&c, 0, sizeof(c));
+  c.x = hidden;
+  c.out = ws + pl.xg;
+  c.targets = targets;
+  c.target_bytes = target_bytes;
+  c.grad_loss = f16 ? grad_loss : nullptr;
+  c.scale = scale;
+  c.out_stride = row;
+  c.tokens = pl.tokens;
+  c.rows = pl.tokens_pad;
+  c.dim = pl.dim;
+  c.vocab = pl.sh.vocab;
+  if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: copy");
+  rr::LogitArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x = hidden;
+  a.x_stride = a.w_stride = dim * pl.esz;
+  if (pack) {
+    a.x = c.out;
+    a.x_stride = a.w_stride = row;
+    if (f16) {
+      // xg is scaled there: the logits need the rows as they are
+      c.out = ws + pl.pack_x;
+      c.targets = nullptr;
+      c.grad_loss = nullptr;
+      c.rows = pl.tokens;
+      if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: copy");
+      a.x = c.out;
+    }
+  }
+  a.kbytes = static_cast<uint32_t>(a.x_stride);
+  a.targets = targets;
+  a.target_bytes = target_bytes;
+  a.lse = lse;
+  a.grad_loss = grad_loss;
+  a.grad = ws + pl.grad;
+  a.tokens = pl.tokens;
+  a.grad_rows = pl.tokens_pad;
+  a.tiles_n = tiles_over(pl.tokens_pad, rr::tile_n(pl.logits_tile));
+  rr::HiddenGradArgs h;
+  memset(&h, 0, sizeof(h));
+  h.grad = a.grad;
+  h.w_stride = a.w_stride;
+  h.acc = reinterpret_cast<float*>(ws + pl.acc);
+  h.split_stride = static_cast<uint64_t>(tokens) * dim;
+  h.tokens = pl.tokens;
+  h.dim = pl.dim;
+  h.grad_rows = pl.tokens_pad;
+  h.tiles_m = tiles_over(dim, rr::tile_m(pl.hidden_tile));
+  h.tiles_n = tiles_over(tokens, rr::tile_n(pl.hidden_tile));
+  h.splits = pl.splits;
+  rr::WeightGradArgs w;
+  memset(&w, 0, sizeof(w));
+  w.grad = a.grad;
+  w.xg = ws + pl.xg;
+  w.xg_stride = row;
+  w.scale = f16 ? scale : nullptr;
+  w.rows = pl.tokens_pad;
+  w.dim = pl.dim;
+  w.tiles_m = tiles_over(dim, rr::tile_m(pl.weight_tile));
+  if (dweights)
+    for (int r = 0; r < p; ++r) w.dw[r] = dweights[r];
+  for (uint32_t c0 = 0; c0 < pl.sh.off[p]; c0 += pl.piece) {
+    const uint32_t c1 = std::min(pl.sh.off[p], c0 + pl.piece);
+    if ((e = vocab_piece(pl, sh, pack, k, c0, c1, ws, a.sh, s)) != hipSuccess)
+      return hip_fail(e, "vocab_cross_entropy_grad: copy");
+    a.c0 = h.c0 = w.c0 = c0;
+    a.c1 = h.c1 = w.c1 = c1;
+    a.ld = h.ld = w.ld = c1 - c0;
+    a.tiles_m = tiles_over(c1 - c0, rr::tile_m(pl.logits_tile));
+    if ((e = rr::launch_logits(a, k, pl.logits_tile, true, s)) != hipSuccess)
+      return hip_fail(e, "vocab_cross_entropy_grad: logits");
+    if (dhidden) {
+      h.sh = a.sh;
+      h.add = c0 > 0 ? 1 : 0;
+      if ((e = rr::launch_hidden_grad(h, k, pl.hidden_tile, s)) != hipSuccess)
+        return hip_fail(e, "vocab_cross_entropy_grad: dhidden");
+    }
+    if (dweights) {
+      w.sh = a.sh;
+      w.tiles_n = tiles_over(c1 - c0, rr::tile_n(pl.weight_tile));
+      if ((e = rr::launch_weight_grad(w, k, pl.weight_tile, s)) != hipSuccess)
+        return hip_fail(e, "vocab_cross_entropy_grad: dweights");
+    }
+  }
+  if (dhidden && tokens > 0) {
+    rr::JoinArgs j;
+    j.acc = h.acc;
+    j.split_stride = h.split_stride;
+    j.grad_loss = f16 ? grad_loss : nullptr;
+    j.targets = targets;
+    j.target_bytes = target_bytes;
+    j.out = dhidden;
+    j.n = static_cast<uint64_t>(tokens) * dim;
+    j.dim = pl.dim;
+    j.splits = pl.splits;
+    j.vocab = pl.sh.vocab;
+    if ((e = rr::launch_join(j, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: dhidden");
+  }
   return ok();
 }
 

@@ -230,6 +230,33 @@ hipError_t launch_ring_exec(const ExecArgs& a, Kind k, rr_op_t op, int per_cu_ca
 // Launches of the ring executor on `device` that stopped on a timed-out wait.
 hipError_t ring_exec_failures(int device, unsigned long long* count);
 
+// Dropout on the way through a collective (rr_dropout.hip).
+enum class DropForm : int {
+  kReduce = 0,   // out[r] = res[r] + D(ring-order fold of in[0..p-1])
+  kScatter = 1,  // out[c] = res[c] + chunk c of D(fold)
+  kGather = 2,   // out[r] = D(in[0], in[1], ... laid end to end)
+  kRanks = 3,    // out[r] = res[r] + D(in[r])
+};
+
+struct DropArgs {
+  const void* in[RR_MAX_RANKS];
+  const void* res[RR_MAX_RANKS];
+  void* out[RR_MAX_RANKS];
+  uint64_t bound[RR_MAX_RANKS + 1];  // the work's chunks: the ring's, or one (kRanks)
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_dev;        // its value is added to offset when the kernel runs (NULL: nothing)
+  uint32_t threshold;                // a word below it drops its element
+  float scale;                       // 1 / (1 - drop)
+  int32_t p;
+  int32_t chunks;
+  int32_t has_res;
+  int32_t one_res;                   // every res[r] is the same buffer
+  int32_t vec;                       // 1: 16-byte accesses
+};
+
+hipError_t launch_dropout(const DropArgs& a, DropForm f, Kind k, hipStream_t stream);
+
 hipError_t launch_fold(const FoldLaunch& f, hipStream_t stream);
 // The phased fold serves same-kind folds on 16-byte-aligned buffers.
 bool phase_supported(const FoldLaunch& f);

@@ -1,0 +1,233 @@
+// rr_vocab_aux.hip -- the vocabulary cross entropy's passes around its matrix
+// products: joining the softmax statistics of the vocabulary's tiles, copying
+// rows into aligned ones, joining split sums.  All are bound by memory and
+// small beside the products.
+#include "rr_device.h"
+#include "rr_vocab.h"
+
+namespace rr {
+
+namespace {
+
+__device__ __forceinline__ bool counts(const void* targets, int bytes, uint32_t i, uint32_t vocab) {
+  const int64_t y = bytes == 8 ? static_cast<const int64_t*>(targets)[i] : static_cast<const int32_t*>(targets)[i];
+  return y >= 0 && y < static_cast<int64_t>(vocab);
+}
+
+// lse = log sum exp over the tiles' (maximum, sum) pairs and the loss lse -
+// target logit.  32 threads share a token, 8 tokens a workgroup, so that one
+// token's few hundred tiles are read by many lanes at once and many tokens'
+// pairs still fill whole 64-byte segments.
+__global__ __launch_bounds__(256) void k_loss(LossArgs a) {
+  __shared__ float sm[32][8][2];
+  const uint32_t ti = threadIdx.x & 7, part = threadIdx.x >> 3;
+  const uint32_t t = blockIdx.x * 8 + ti;
+  float mx = -__builtin_inff(), sum = 0.f;
+  if (t < a.tokens) {
+    for (uint32_t i = part; i < a.tiles; i += 32) {
+      const float2 v = *reinterpret_cast<const float2*>(a.part + (static_cast<uint64_t>(i) * a.tokens + t) * 2);
+      const float top = fmaxf(mx, v.x);
+      const float ref = top == -__builtin_inff() ? 0.f : top;
+      sum = sum * __expf(mx - ref) + v.y * __expf(v.x - ref);
+      mx = top;
+    }
+  }
+  sm[part][ti][0] = mx;
+  sm[part][ti][1] = sum;
+  __syncthreads();
+  for (uint32_t h = 16; h > 0; h >>= 1) {
+    if (part < h) {
+      const float m2 = sm[part + h][ti][0], s2 = sm[part + h][ti][1];
+      const float top = fmaxf(mx, m2);
+      const float ref = top == -__builtin_inff() ? 0.f : top;
+      sum = sum * __expf(mx - ref) + s2 * __expf(m2 - ref);
+      mx = top;
+      sm[part][ti][0] = mx;
+      sm[part][ti][1] = sum;
+    }
+    __syncthreads();
+  }
+  if (part == 0 && t < a.tokens) {
+    const float lse = mx + logf(sum);
+    a.lse[t] = lse;
+    a.loss[t] = counts(a.targets, a.target_bytes, t, a.vocab) ? lse - a.hit[t] : 0.f;
+  }
+}
+
+// One workgroup: the largest finite |grad_loss| of the tokens that count (1 if
+// there is none but zeros).
+__global__ __launch_bounds__(1024) void k_grad_scale(const float* g, const void* targets, int target_bytes,
+                                                     uint32_t tokens, uint32_t vocab, float* scale) {
+  __shared__ float sm[16];
+  float mx = 0.f;
+  for (uint32_t i = threadIdx.x; i < tokens; i += 1024) {
+    const float v = fabsf(g[i]);
+    if (v < __builtin_inff() && counts(targets, target_bytes, i, vocab)) mx = fmaxf(mx, v);
+  }
+  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = mx;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sm[i]);
+    *scale = mx > 0.f ? mx : 1.f;
+  }
+}
+
+// 16 bytes of a row from element d on, zeros from `dim` on.
+template <class S>
+__device__ __forceinline__ void read_chunk(const S* row, uint32_t d, uint32_t dim, bool vec, S* out) {
+  constexpr uint32_t EPC = 16 / sizeof(S);
+  if (vec) {
+    *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(row + d);
+  } else {
+#pragma unroll
+    for (uint32_t j = 0; j < EPC; ++j) out[j] = d + j < dim ? row[d + j] : S(0);
+  }
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void k_pack_rows(PackRowsArgs a) {
+  using S = typename E::S;
+  constexpr uint32_t EPC = 16 / sizeof(S);
+  const uint32_t t = blockIdx.x;
+  const bool live = t < a.tokens && (!a.targets || counts(a.targets, a.target_bytes, t, a.vocab));
+  float f = 1.f;
+  bool scaled = false;
+  if (a.grad_loss && live) {
+    const float g = a.grad_loss[t];
+    // float16: g relative to the largest, so that the product stays in the
+    // type's range; equal weights scale by exactly 1 and add no rounding
+    f = fabsf(g) < __builtin_inff() ? g / a.scale[0] : g;
+    scaled = f != 1.f;
+  }
+  const S* row = static_cast<const S*>(a.x) + static_cast<uint64_t>(t) * a.dim;
+  const bool vec = a.dim % EPC == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
+  char* out = static_cast<char*>(a.out) + t * a.out_stride;
+  for (uint32_t d = threadIdx.x * EPC; d < a.dim; d += 256 * EPC) {
+    __attribute__((aligned(16))) S v[EPC];
+    if (live) {
+      read_chunk<S>(row, d, a.dim, vec, v);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < EPC; ++j) v[j] = S(0);
+    }
+    if constexpr (__is_same(E, EF16)) {
+      if (scaled) {
+#pragma unroll
+        for (uint32_t j = 0; j < EPC; ++j) v[j] = static_cast<S>(f32_to_f16_bits(f16_bits_to_f32(v[j]) * f));
+      }
+    }
+    *reinterpret_cast<u32x4*>(out + d * sizeof(S)) = *reinterpret_cast<const u32x4*>(v);
+  }
+}
+
+template <class S>
+__global__ __launch_bounds__(256) void k_pack_weight(PackWeightArgs a) {
+  constexpr uint32_t EPC = 16 / sizeof(S);
+  const uint32_t c = a.c0 + blockIdx.x;
+  const S* row = nullptr;
+  for (int r = 0; r < a.sh.p; ++r)
+    if (c >= a.sh.off[r] && c - a.sh.off[r] < a.sh.rows[r])
+      row = static_cast<const S*>(a.sh.w[r]) + static_cast<uint64_t>(c - a.sh.off[r]) * a.dim;
+  char* out = static_cast<char*>(a.out) + blockIdx.x * a.out_stride;
+  for (uint32_t d = threadIdx.x * EPC; d < a.dim; d += 256 * EPC) {
+    __attribute__((aligned(16))) S v[EPC];
+    if (row) {
+      read_chunk<S>(row, d, a.dim, false, v);
+    } else {
+#pragma unroll
+      for (uint32_t j = 0; j < EPC; ++j) v[j] = S(0);
+    }
+    *reinterpret_cast<u32x4*>(out + d * sizeof(S)) = *reinterpret_cast<const u32x4*>(v);
+  }
+}
+
+// dhidden = the sum of the splits' float32 accumulators, rounded once.  A
+// masked token's row is zero whatever the weights hold.
+template <class E>
+__global__ __launch_bounds__(256) void k_join(JoinArgs a) {
+  using S = typename E::S;
+  const uint32_t t = blockIdx.x;
+  const bool live = counts(a.targets, a.target_bytes, t, a.vocab);
+  const float f = a.grad_loss && live ? a.grad_loss[t] * (1.f / 32768.f) : 1.f;
+  const uint64_t base = static_cast<uint64_t>(t) * a.dim;
+  S* out = static_cast<S*>(a.out) + base;
+  for (uint32_t d = threadIdx.x; d < a.dim; d += 256) {
+    float v = 0.f;
+    if (live) {
+      v = a.acc[base + d];
+      for (uint32_t s = 1; s < a.splits; ++s) v += a.acc[s * a.split_stride + base + d];
+      v *= f;
+    }
+    store_one<E>(out + d, v);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_loss(const LossArgs& a, hipStream_t s) {
+  if (a.tokens == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_loss, dim3((a.tokens + 7) / 8), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const float* grad_loss, const void* targets, int target_bytes, uint32_t tokens,
+                             uint32_t vocab, float* scale, hipStream_t s) {
+  hipLaunchKernelGGL(k_grad_scale, dim3(1), dim3(1024), 0, s, grad_loss, targets, target_bytes, tokens, vocab, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_pack_rows(const PackRowsArgs& a, Kind k, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  switch (k) {
+    case Kind::kF32: hipLaunchKernelGGL(k_pack_rows<EF32>, dim3(a.rows), dim3(256), 0, s, a); break;
+    case Kind::kBF16: hipLaunchKernelGGL(k_pack_rows<EBF16>, dim3(a.rows), dim3(256), 0, s, a); break;
+    default: hipLaunchKernelGGL(k_pack_rows<EF16>, dim3(a.rows), dim3(256), 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_pack_weight(const PackWeightArgs& a, Kind k, hipStream_t s) {
+  const dim3 g(a.c1 - a.c0);
+  if (k == Kind::kF32)
+    hipLaunchKernelGGL(k_pack_weight<uint32_t>, g, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(k_pack_weight<uint16_t>, g, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_join(const JoinArgs& a, Kind k, hipStream_t s) {
+  const dim3 g(static_cast<uint32_t>(a.n / a.dim));
+  if (g.x == 0) return hipSuccess;
+  switch (k) {
+    case Kind::kF32: hipLaunchKernelGGL(k_join<EF32>, g, dim3(256), 0, s, a); break;
+    case Kind::kBF16: hipLaunchKernelGGL(k_join<EBF16>, g, dim3(256), 0, s, a); break;
+    default: hipLaunchKernelGGL(k_join<EF16>, g, dim3(256), 0, s, a); break;
+  }
+  return hipGetLastError();
+}
+
+#define RR_DISPATCH(CALL)                 \
+  switch (k) {                            \
+    case Kind::kF32: return CALL(f32);    \
+    case Kind::kBF16: return CALL(bf16);  \
+    default: return CALL(f16);            \
+  }
+
+hipError_t launch_logits(const LogitArgs& a, Kind k, VocabTile t, bool grad, hipStream_t s) {
+#define RR_CALL(NAME) launch_logits_##NAME(a, t, grad, s)
+  RR_DISPATCH(RR_CALL)
+#undef RR_CALL
+}
+hipError_t launch_hidden_grad(const HiddenGradArgs& a, Kind k, VocabTile t, hipStream_t s) {
+#define RR_CALL(NAME) launch_hidden_grad_##NAME(a, t, s)
+  RR_DISPATCH(RR_CALL)
+#undef RR_CALL
+}
+hipError_t launch_weight_grad(const WeightGradArgs& a, Kind k, VocabTile t, hipStream_t s) {
+#define RR_CALL(NAME) launch_weight_grad_##NAME(a, t, s)
+  RR_DISPATCH(RR_CALL)
+#undef RR_CALL
+}
+
+}  // namespace rr

@@ -392,6 +392,133 @@ rr_status_t rr_reduce_scatter_dim1(const void* const* sendbufs, void* const* rec
                                    size_t cols, rr_dtype_t dtype, rr_op_t op, rr_stream_t stream);
 
 /*
+ * Dropout from a counter-based generator on the way through a collective
+ * (float32, bfloat16 and float16; int32 -> RR_ERROR_UNSUPPORTED).
+ *   D(v)_i = word(i) >= floor(drop * 2^32) ? v * (1 / (1 - drop)) : +0, where
+ *   word(i) is word i mod 4 of Philox4x32-10 (Salmon, Moraes, Dror, Shaw,
+ *   "Parallel random numbers: as easy as 1, 2, 3", SC 2011) with the 64-bit
+ *   key `seed` and the 128-bit counter (floor(i / 4), offset), low halves
+ *   first.  i is the element's index in the full vector of n elements, so
+ *   every rank, every form below and every dtype draws one mask for one
+ *   (seed, offset), and no mask is stored.  A dropped element contributes +0
+ *   whatever its value (infinities and NaN included).
+ *   drop: 0 <= drop < 1 (0 keeps every element unscaled).  The scale is
+ *     rounded once to float32.
+ *   offset: a number of the caller's own for each use of a seed (layer, step):
+ *     calls that share (seed, offset) share their mask.
+ *   offset_dev: device pointer to a 64-bit number, 8-byte aligned, that is
+ *     added to offset when the kernel runs, or NULL.  A captured graph replays its
+ *     arguments unchanged; a counter behind offset_dev that the graph or the
+ *     caller advances gives every replay its own mask.
+ * Arithmetic: the fold of the collective in float32, times the scale (one
+ * rounding), plus the widened residual (one rounding), converted once.
+ */
+typedef struct {
+  double drop;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* offset_dev;
+} rr_dropout_t;
+
+/*
+ * Row-parallel output [TP]: all-reduce, dropout and residual addition in one
+ * pass: recvbufs[r] = residuals[r] + D(x_0 + ... + x_{p-1}) (ring order per
+ * chunk, as rr_all_reduce).
+ *   residuals: NULL (nothing is added) or p buffers of n elements, which may
+ *   all be the same buffer.  In place allowed: recvbufs[r] == sendbufs[r], and
+ *   recvbufs[r] == residuals[r] if no other rank's residual is that buffer.
+ *   A layer's bias belongs into one rank's partial output.
+ * Gradient: of the residuals, the outputs' gradients themselves; of every
+ *   input, D(sum over r of dy_r) -- this call on the dy_r without residuals -- or,
+ *   where each rank's dy_r already is the gradient of the one loss (tensor
+ *   parallelism: the ranks' outputs are copies), D(dy_r): rr_dropout.
+ */
+rr_status_t rr_all_reduce_dropout(const void* const* sendbufs, const void* const* residuals, void* const* recvbufs,
+                                  int p, size_t n, rr_dtype_t dtype, rr_dropout_t drop, rr_stream_t stream);
+
+/*
+ * The sequence-sharded form: rank c receives chunk c of D(sum) plus its own
+ * residual: recvbufs[c][j] = residuals[c][j] + D(sum)[c*(n/p) + j].
+ *   residuals: NULL or p buffers of n/p elements.  Requires p | n.  In place
+ *   as rr_reduce_scatter, or recvbufs[c] == residuals[c] (as above).
+ * Gradient of every input: rr_all_gather_dropout of the outputs' gradients.
+ */
+rr_status_t rr_reduce_scatter_dropout(const void* const* sendbufs, const void* const* residuals,
+                                      void* const* recvbufs, int p, size_t n, rr_dtype_t dtype, rr_dropout_t drop,
+                                      rr_stream_t stream);
+
+/*
+ * Rank by rank, no sum: recvbufs[r] = residuals[r] + D(sendbufs[r]), n elements
+ * each, the same mask for every rank (drawn once for all of them).  Aliasing as
+ * rr_all_reduce_dropout.
+ */
+rr_status_t rr_dropout(const void* const* sendbufs, const void* const* residuals, void* const* recvbufs, int p,
+                       size_t n, rr_dtype_t dtype, rr_dropout_t drop, rr_stream_t stream);
+
+/*
+ * recvbufs[r][c*(n/p) + j] = D(the shards laid end to end)[c*(n/p) + j]: an
+ * all-gather that drops its values on the way.  Requires p | n.  In place as
+ * rr_all_gather.
+ */
+rr_status_t rr_all_gather_dropout(const void* const* sendbufs, void* const* recvbufs, int p, size_t n,
+                                  rr_dtype_t dtype, rr_dropout_t drop, rr_stream_t stream);
+
+/*
+ * Softmax cross entropy against a vocabulary cut over the ranks [TP], without
+ * keeping the [tokens, vocab] logits (float32, bfloat16 and float16).
+ *   z_tv = sum_k hidden[t][k] * w_v[k];  lse_t = log sum_v exp(z_tv);
+ *   loss[t] = lse_t - z_{t, target_t}.
+ *   weights[r]: rank r's rows of the output weight, a row-major [V_r, dim]
+ *     matrix of the vocabulary's rows floor(r*vocab/p) .. floor((r+1)*vocab/p)
+ *     (the chunk bounds above; a rank without rows may be NULL).
+ *   hidden: [tokens, dim], row-major: the hidden states, which every rank holds
+ *     alike; one copy serves the p virtual ranks.
+ *   targets: one index per token in the whole vocabulary, int32 or int64
+ *     (target_bytes 4 or 8).  A target outside [0, vocab) marks a masked token:
+ *     its loss is 0 and nothing depends on it.
+ *   loss, lse: float32, [tokens].
+ *   workspace: as in rr_all_reduce_ex; rr_vocab_cross_entropy_workspace_size()
+ *     bytes.  Its contents mean nothing between calls.
+ *   1 <= dim <= 2^20, 1 <= vocab <= 2^23, tokens <= 2^23, tokens*dim and
+ *   vocab*dim <= 2^36.  Rows of a multiple of 16 bytes in 16-byte aligned
+ *   buffers are read in place; others are copied into aligned rows of the
+ *   workspace first, a part of the vocabulary at a time.
+ * Arithmetic: products of the storage type summed in float32 on the matrix
+ * cores; maximum, sum and loss in float32.  A row of logits with +inf gives NaN.
+ * No output may overlap an input, another output or the workspace.
+ */
+rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weights, const void* targets,
+                                   int target_bytes, float* loss, float* lse, int p, size_t tokens, size_t dim,
+                                   size_t vocab, rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                   rr_stream_t stream);
+
+/*
+ * Its gradient for the gradients grad_loss[t] (float32) of the losses:
+ *   g_tv = grad_loss[t] * (exp(z_tv - lse_t) - [v = target_t]), 0 for masked tokens;
+ *   dhidden[t] = sum_v g_tv * w_v, summed over the ranks' shards;
+ *   dweights[r][v] = sum_t g_tv * hidden[t].
+ *   lse: what rr_vocab_cross_entropy wrote for the same inputs.
+ *   dhidden: [tokens, dim], or NULL; dweights: p matrices shaped as weights, or
+ *     NULL; not both NULL.  With tokens == 0 dweights is filled with zeros.
+ * Arithmetic: the logits are computed again; g is rounded once to the storage
+ * type (float16: as a probability times 2^15, and the hidden rows are scaled by
+ * grad_loss / max |grad_loss| in float16 for dweights), the products are summed
+ * in float32 and rounded once.  The same inputs give the same bits every time.
+ */
+rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* weights, const void* targets,
+                                        int target_bytes, const float* lse, const float* grad_loss, void* dhidden,
+                                        void* const* dweights, int p, size_t tokens, size_t dim, size_t vocab,
+                                        rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                        rr_stream_t stream);
+
+/* Workspace bytes of rr_vocab_cross_entropy (grad = 0) and
+ * rr_vocab_cross_entropy_grad (grad != 0); 0 for invalid arguments.  The
+ * gradient keeps one part of the logits' gradient at a time, at most 256 MiB
+ * (or 256 columns). */
+size_t rr_vocab_cross_entropy_workspace_size(int p, size_t tokens, size_t dim, size_t vocab, rr_dtype_t dtype,
+                                             int grad);
+
+/*
  * Workspace bytes that rr_all_reduce_ex needs for (algo, p, group_size, n,
  * dtype): 0 for the fused algorithms and for the staged ring on int32/float32;
  * p*n*4 for the staged ring on bfloat16 and float16; (p/group_size) times

@@ -1,0 +1,344 @@
+"""The vocabulary-parallel cross entropy on the GPU against the definition in
+float64.
+
+Tolerances, with u = eps/2 of the storage type and f = 2^-23 (one unit of a
+float32 sum, rounded or truncated):
+  logit: a sum of d exact products: |dz| <= (d + 2) f sum_k |h_k w_k| =: Z
+    (largest over the row's columns);
+  lse: |d lse| <= Z + 16 f (log V + |lse| + 4) =: L -- each exponential is off
+    by (|argument| + 4) f, weighted by its probability, and the statistics are
+    merged a few times; the loss adds one logit and a rounding;
+  gradient of a logit: g (p (Z + L + 4 f) + u |p - onehot|), then sums over V (or
+    T) terms: (terms + 2) f of the sum of the magnitudes, and u of the result;
+    float16 adds u for the scaled hidden rows and its subnormal steps.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import training as TR
+from oracle.collectives import chunk_bounds
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"float32": torch.float32, "bfloat16": torch.bfloat16, "float16": torch.float16}
+F = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def rr():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import collective_communication_reduction_way_amd as mod
+
+    mod.lib()
+    return mod
+
+
+def inputs(seed, p, T, d, V, dtype, masked=0.2, shift=0):
+    """Hidden states, shards (each `shift` elements past a 16-byte boundary), targets, loss gradients."""
+    rng = np.random.default_rng([seed, p, T, d, V])
+    w = torch.from_numpy(rng.standard_normal((V, d)) * 1.5 / np.sqrt(d)).to(DT[dtype])
+    t = rng.integers(0, V, size=T)
+    h = rng.standard_normal((T, d))
+    h[::2] += 2.0 * w.double().numpy()[t[::2]]
+    t[rng.random(T) < masked] = -100
+    h = torch.from_numpy(h).to(DT[dtype])
+    g = torch.from_numpy(rng.uniform(-1.5, 1.5, size=T)).float()
+
+    def put(x):
+        buf = torch.empty(x.numel() + shift, dtype=x.dtype, device="cuda")
+        buf[shift:].copy_(x.reshape(-1).cuda())
+        return buf[shift:].view(x.shape)
+
+    b = chunk_bounds(V, p)
+    return put(h), [put(w[b[r]:b[r + 1]].contiguous()) for r in range(p)], torch.from_numpy(t).cuda(), g.cuda()
+
+
+def bounds(h, w, t, g, dtype):
+    """Float64 results and their tolerances."""
+    h, t = h.double().cpu().numpy(), t.cpu().numpy().astype(np.int64)
+    w = torch.cat([x.double().cpu() for x in w]).numpy()
+    g = g.double().cpu().numpy()
+    T, d = h.shape
+    V = w.shape[0]
+    u = torch.finfo(DT[dtype]).eps / 2
+    loss, lse, dh, dw = TR.cross_entropy(h, w, t, g)
+    live = (t >= 0) & (t < V)
+    Z = ((d + 2) * F * (np.abs(h) @ np.abs(w).T)).max(axis=1) if T else np.zeros(0)
+    L = Z + 16 * F * (np.log(V) + np.abs(lse) + 4)
+    tl = np.where(live, Z + L + 2 * F * np.abs(loss), 0.0)
+    ga = np.where(live, np.abs(g), 0.0)
+    P = np.exp(h @ w.T - lse[:, None])
+    hot = np.zeros_like(P)
+    hot[np.arange(T)[live], t[live]] = 1
+    # an fp16 gradient entry of a logit has steps of 2^-24 at 2^15 times its size
+    tiny = 2.0 ** -39 if dtype == "float16" else 0.0
+    dG = ga[:, None] * (P * (Z + L + 4 * F)[:, None] + 2 * u * np.abs(P - hot) + tiny)
+    G = ga[:, None] * np.abs(P - hot)
+    out_tiny = 2.0 ** -24 if dtype == "float16" else 0.0
+    th = dG @ np.abs(w) + (V + 2) * F * (G @ np.abs(w)) + u * np.abs(dh) + out_tiny
+    hz = np.where(live[:, None], np.abs(h), 0.0)
+    xtra = (u * (G.T @ hz) + 2.0 ** -25 * ga.max(initial=0.0) * np.abs(P - hot).T @ live[:, None]
+            if dtype == "float16" else 0.0)
+    tw = dG.T @ hz + (T + 2) * F * (G.T @ hz) + u * np.abs(dw) + out_tiny + xtra
+    return (loss, lse, dh, dw), (tl, L, th, tw)
+
+
+def check(got, want, tol, what):
+    got = got.double().cpu().numpy()
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    assert np.isfinite(got).all(), what
+    over = np.abs(got - want) - tol
+    if over.size and over.max() > 0:
+        i = np.unravel_index(over.argmax(), over.shape)
+        raise AssertionError(f"{what}: {(over > 0).sum()} of {over.size} off, worst at {i}: got {got[i]} want {want[i]} tol "
+                             f"{np.broadcast_to(tol, over.shape)[i]}")
+
+
+def run_and_check(rr, p, T, d, V, dtype, seed=1, masked=0.2, shift=0, int32=False):
+    h, w, t, g = inputs(seed, p, T, d, V, dtype, masked, shift)
+    if int32:
+        t = t.int()
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    want, tol = bounds(h, w, t, g, dtype)
+    check(loss, want[0], tol[0], "loss")
+    check(lse, want[1], tol[1], "lse")
+    check(dh, want[2], tol[2], "dhidden")
+    check(torch.cat(dw), want[3], tol[3], "dweights")
+    return (h, w, t, g), (loss, lse, dh, dw)
+
+
+SHAPES = [
+    # p, tokens, dim, vocab
+    (1, 1, 64, 100), (1, 1, 8, 1), (2, 1, 768, 5003), (3, 7, 72, 1000), (4, 32, 128, 777), (8, 33, 256, 1031),
+    (5, 63, 520, 300), (1, 64, 64, 64), (2, 65, 200, 4099), (8, 129, 384, 2048), (3, 300, 136, 900), (7, 257, 64, 515),
+    (64, 40, 64, 333), (6, 20, 64, 4), (2, 512, 512, 2500),
+]
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("p,T,d,V", SHAPES)
+def test_against_the_definition(rr, p, T, d, V, dtype):
+    run_and_check(rr, p, T, d, V, dtype)
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("p,T,d,V,shift", [(2, 5, 1, 40, 0), (3, 33, 77, 501, 0), (1, 70, 333, 1500, 0), (4, 40, 64, 600, 1),
+                                           (2, 100, 130, 700, 3)])
+def test_rows_that_are_not_aligned(rr, p, T, d, V, shift, dtype):
+    run_and_check(rr, p, T, d, V, dtype, shift=shift, int32=True)
+
+
+@pytest.mark.parametrize("dtype", ("bfloat16", "float32"))
+def test_large_tiles(rr, dtype):
+    """Enough tiles for the largest tile of every product."""
+    run_and_check(rr, 3, 2100, 2064, 8300, dtype, seed=5)
+
+
+def test_all_tokens_masked(rr):
+    h, w, t, g = inputs(2, 3, 50, 64, 500, "bfloat16")
+    t.fill_(-100)
+    h.fill_(float("nan"))
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    assert (loss == 0).all() and (dh == 0).all() and all((x == 0).all() for x in dw)
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("d", (64, 70))
+def test_masked_rows_hold_anything(rr, dtype, d):
+    """NaN and infinities in masked tokens' hidden rows, loss gradients and
+    statistics change nothing elsewhere; targets far outside count as masked."""
+    h, w, t, g = inputs(3, 2, 90, d, 700, dtype)
+    t[5], t[6], t[7] = 700, -2 ** 40, 2 ** 40
+    clean = rr.vocab_cross_entropy(h, w, t)
+    want = rr.vocab_cross_entropy_grad(h, w, t, clean[1], g)
+    dead = (t < 0) | (t >= 700)
+    h2, g2 = h.clone(), g.clone()
+    h2[dead] = float("nan")
+    h2[6] = float("inf")
+    g2[dead] = float("inf")
+    loss, lse = rr.vocab_cross_entropy(h2, w, t)
+    assert torch.equal(loss, clean[0]) and torch.equal(lse[~dead], clean[1][~dead])
+    got = rr.vocab_cross_entropy_grad(h2, w, t, lse, g2)
+    assert torch.equal(got[0], want[0]) and all(torch.equal(a, b) for a, b in zip(got[1], want[1]))
+    assert (got[0][dead] == 0).all()
+
+
+def test_no_tokens(rr):
+    h, w, t, g = inputs(4, 3, 0, 64, 500, "bfloat16")
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    assert loss.numel() == lse.numel() == 0
+    dws = [torch.full_like(x, float("nan")) for x in w]
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g, dweights=dws)
+    assert dh.numel() == 0 and all((x == 0).all() for x in dw)
+
+
+def test_extreme_logits(rr):
+    """Logits of +-1e4: the sums stay finite and the loss is the difference of two logits."""
+    h = torch.zeros(40, 64, device="cuda")
+    h[:, 0] = 100.0
+    w = torch.zeros(300, 64, device="cuda")
+    w[7, 0], w[9, 0], w[11, 0] = 100.0, 99.0, -100.0
+    t = torch.full((40,), 9, device="cuda")
+    t[1] = 7
+    t[2] = 11
+    loss, lse = rr.vocab_cross_entropy(h, [w], t)
+    assert (lse == 10000.0).all() and loss[0] == 100.0 and loss[1] == 0.0 and loss[2] == 20000.0
+    dh, dw = rr.vocab_cross_entropy_grad(h, [w], t, lse, torch.ones(40, device="cuda"))
+    assert torch.equal(dh[0], w[7] - w[9]) and (dh[1] == 0).all() and torch.equal(dh[2], w[7] - w[11])
+    assert dw[0][11, 0] == -100.0 and (dw[0][12] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
+def test_ranks_are_only_where_rows_lie(rr, dtype):
+    """One shard or eight: the same losses and gradients within twice the tolerance."""
+    h, w, t, g = inputs(6, 8, 150, 128, 3000, dtype)
+    one = [torch.cat(w)]
+    want, tol = bounds(h, w, t, g, dtype)
+    for ws in (w, one):
+        loss, lse = rr.vocab_cross_entropy(h, ws, t)
+        dh, dw = rr.vocab_cross_entropy_grad(h, ws, t, lse, g)
+        for got, a, b, what in zip((loss, lse, dh, torch.cat(dw)), want, tol, ("loss", "lse", "dhidden", "dweights")):
+            check(got, a, b, what)
+
+
+def test_float16_gradients_of_uneven_tokens(rr):
+    """Loss gradients over twelve orders of magnitude: every row keeps its own precision in dhidden."""
+    h, w, t, g = inputs(7, 2, 60, 128, 2000, "float16", masked=0.0)
+    g = torch.logspace(-6, 3, 60, device="cuda")
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    want, tol = bounds(h, w, t, g, "float16")
+    check(dh, want[2], tol[2], "dhidden")
+    check(torch.cat(dw), want[3], tol[3], "dweights")
+
+
+def test_gradient_against_differences(rr):
+    """Float32, along random directions: the loss is smooth, so a central
+    difference over +-e is off by e^2 times the third derivative (under 10 here) and by
+    the losses' own error over e."""
+    h, w, t, g = inputs(8, 2, 37, 64, 300, "float32")
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    total = lambda a, b: float((rr.vocab_cross_entropy(a, b, t)[0].double() * g.double()).sum())
+    e = 2.0 ** -6
+    _, tol = bounds(h, w, t, g, "float32")
+    err = 2 * float((tol[0] * g.abs().double().cpu().numpy()).sum()) / (2 * e) + 37 * 1.5 * 10 * e * e
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    v = torch.randn(h.shape, generator=gen, device="cuda")
+    v /= v.norm(dim=1, keepdim=True)
+    got = (total(h + e * v, w) - total(h - e * v, w)) / (2 * e)
+    assert abs(got - float((dh.double() * v.double()).sum())) <= err
+    v = torch.randn(w[1].shape, generator=gen, device="cuda")
+    v /= v.norm() * 3
+    got = (total(h, [w[0], w[1] + e * v]) - total(h, [w[0], w[1] - e * v])) / (2 * e)
+    assert abs(got - float((dw[1].double() * v.double()).sum())) <= err
+
+
+def test_one_side_only_and_same_bits(rr):
+    h, w, t, g = inputs(9, 3, 100, 192, 1500, "bfloat16")
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    a = rr.vocab_cross_entropy_grad(h, w, t, lse, g, need_weights=False)
+    b = rr.vocab_cross_entropy_grad(h, w, t, lse, g, need_hidden=False)
+    assert a[1] is None and b[0] is None
+    assert torch.equal(a[0], dh) and all(torch.equal(x, y) for x, y in zip(b[1], dw))
+    again = rr.vocab_cross_entropy(h, w, t)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+
+
+def test_other_stream_and_graph(rr):
+    h, w, t, g = inputs(10, 4, 200, 128, 2500, "bfloat16")
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    l2, s2 = rr.vocab_cross_entropy(h, w, t, stream=side)
+    dh2, dw2 = rr.vocab_cross_entropy_grad(h, w, t, s2, g, stream=side)
+    side.synchronize()
+    assert torch.equal(l2, loss) and torch.equal(dh2, dh) and all(torch.equal(a, b) for a, b in zip(dw2, dw))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        l3, s3 = rr.vocab_cross_entropy(h, w, t)
+        dh3, dw3 = rr.vocab_cross_entropy_grad(h, w, t, s3, g)
+    for k in range(3):
+        h.mul_(0.5 if k else 1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        loss, lse = rr.vocab_cross_entropy(h, w, t)
+        dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+        assert torch.equal(l3, loss) and torch.equal(s3, lse), k
+        assert torch.equal(dh3, dh) and all(torch.equal(a, b) for a, b in zip(dw3, dw)), k
+
+
+def test_workspace_may_hold_anything(rr):
+    h, w, t, g = inputs(11, 2, 70, 66, 900, "bfloat16")
+    want = rr.vocab_cross_entropy(h, w, t)
+    wgrad = rr.vocab_cross_entropy_grad(h, w, t, want[1], g)
+    for fill in (0, 0x7F, 0xFF):
+        ws = torch.full((rr.vocab_cross_entropy_workspace_size(2, 70, 66, 900, "bfloat16"),), fill, dtype=torch.uint8,
+                        device="cuda")
+        got = rr.vocab_cross_entropy(h, w, t, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        ws = torch.full((rr.vocab_cross_entropy_workspace_size(2, 70, 66, 900, "bfloat16", grad=True),), fill,
+                        dtype=torch.uint8, device="cuda")
+        got = rr.vocab_cross_entropy_grad(h, w, t, want[1], g, workspace=ws)
+        assert torch.equal(got[0], wgrad[0]) and all(torch.equal(a, b) for a, b in zip(got[1], wgrad[1]))
+
+
+def test_several_pieces(rr):
+    """So many tokens that the vocabulary is walked in pieces: the float64
+    definition on the GPU, error relative to the gradients' norm (each of a
+    few bf16 roundings, at most 2^-8 each)."""
+    T, d, V, p = 70000, 64, 5000, 3
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    h = torch.randn(T, d, generator=gen, device="cuda").bfloat16()
+    w = (torch.randn(V, d, generator=gen, device="cuda") * 0.2).bfloat16()
+    b = chunk_bounds(V, p)
+    ws = [w[b[r]:b[r + 1]].contiguous() for r in range(p)]
+    t = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    g = torch.rand(T, generator=gen, device="cuda") / T
+    loss, lse = rr.vocab_cross_entropy(h, ws, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, ws, t, lse, g)
+    z = h.double() @ w.double().t()
+    wl = torch.logsumexp(z, dim=1)
+    assert ((lse.double() - wl).abs() < 1e-4).all()
+    z = torch.exp(z - wl[:, None])
+    z[torch.arange(T, device="cuda"), t] -= 1
+    z *= g.double()[:, None]
+    want_h, want_w = z @ w.double(), z.t() @ h.double()
+    del z
+    for got, want in ((dh, want_h), (torch.cat(dw), want_w)):
+        assert float((got.double() - want).norm() / want.norm()) < 2 * 2.0 ** -8
+    torch.cuda.empty_cache()
+
+
+def test_training_step_end_to_end(rr):
+    """The two ends together: a row-parallel output (dropout, residual) into the
+    loss, and the gradients back to every rank's partial output."""
+    p, T, d, V, dtype = 4, 96, 128, 1000, "bfloat16"
+    h, w, t, g = inputs(12, p, T, d, V, dtype)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    parts = torch.randn(p, T * d, generator=gen, device="cuda").bfloat16()
+    res = h.reshape(-1)
+    outs = torch.empty_like(parts)
+    rr.all_reduce_dropout(parts, outs, drop=0.1, seed=5, offset=6, residuals=[res] * p)
+    assert all(torch.equal(outs[0], outs[r]) for r in range(p))
+    y = outs[0].view(T, d)
+    loss, lse = rr.vocab_cross_entropy(y, w, t)
+    dy, dw = rr.vocab_cross_entropy_grad(y, w, t, lse, g)
+    want, tol = bounds(y, w, t, g, dtype)
+    check(loss, want[0], tol[0], "loss")
+    check(dy, want[2], tol[2], "dhidden")
+    check(torch.cat(dw), want[3], tol[3], "dweights")
+    copies = torch.empty_like(parts)
+    rr.broadcast(dy.reshape(-1), copies)
+    dparts = torch.empty_like(parts)
+    rr.dropout(copies, dparts, drop=0.1, seed=5, offset=6)
+    keep = torch.from_numpy(TR.dropout_keep(T * d, 0.1, 5, 6)).cuda()
+    want = torch.where(keep, dy.reshape(-1).float() * np.float32(1 / 0.9), torch.zeros((), device="cuda")).bfloat16()
+    assert all(torch.equal(dparts[r], want) for r in range(p))
