@@ -1465,7 +1465,6 @@ rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weight
     c.out_stride = static_cast<uint64_t>(pl.dim_pad) * pl.esz;
     c.tokens = c.rows = pl.tokens;
     c.dim = pl.dim;
-    c.vocab = pl.sh.vocab;
     if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy: copy");
     a.x = c.out;
     a.x_stride = a.w_stride = c.out_stride;
@@ -1551,7 +1550,9 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   rr::VocabShards sh = pl.sh;
   for (int r = 0; r < p; ++r) sh.w[r] = weights[r];
   hipError_t e = hipSuccess;
-  float* scale = reinterpret_cast<float*>(ws + pl.scale);
+  int32_t* scale = reinterpret_cast<int32_t*>(ws + pl.scale);
+  uint32_t* tcol = reinterpret_cast<uint32_t*>(ws + pl.tcol);
+  float* lo = reinterpret_cast<float*>(ws + pl.lo);
   if (f16) {
     e = rr::launch_grad_scale(grad_loss, targets, target_bytes, pl.tokens, pl.sh.vocab, scale, s);
     if (e != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: scale");
@@ -1566,11 +1567,12 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   c.target_bytes = target_bytes;
   c.grad_loss = f16 ? grad_loss : nullptr;
   c.scale = scale;
+  c.sh = sh;
+  c.tcol = tcol;
   c.out_stride = row;
   c.tokens = pl.tokens;
   c.rows = pl.tokens_pad;
   c.dim = pl.dim;
-  c.vocab = pl.sh.vocab;
   if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: copy");
   rr::LogitArgs a;
   memset(&a, 0, sizeof(a));
@@ -1583,6 +1585,7 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
       // xg is scaled there: the logits need the rows as they are
       c.out = ws + pl.pack_x;
       c.targets = nullptr;
+      c.tcol = nullptr;
       c.grad_loss = nullptr;
       c.rows = pl.tokens;
       if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: copy");
@@ -1595,6 +1598,8 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   a.lse = lse;
   a.grad_loss = grad_loss;
   a.grad = ws + pl.grad;
+  a.tcol = tcol;
+  a.lo = lo;
   a.tokens = pl.tokens;
   a.grad_rows = pl.tokens_pad;
   a.tiles_n = tiles_over(pl.tokens_pad, rr::tile_n(pl.logits_tile));
@@ -1616,6 +1621,9 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   w.xg = ws + pl.xg;
   w.xg_stride = row;
   w.scale = f16 ? scale : nullptr;
+  w.tcol = tcol;
+  w.lo = lo;
+  w.tokens = pl.tokens;
   w.rows = pl.tokens_pad;
   w.dim = pl.dim;
   w.tiles_m = tiles_over(dim, rr::tile_m(pl.weight_tile));
@@ -1646,16 +1654,16 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   }
   if (dhidden && tokens > 0) {
     rr::JoinArgs j;
+    j.sh = sh;
     j.acc = h.acc;
     j.split_stride = h.split_stride;
     j.grad_loss = f16 ? grad_loss : nullptr;
-    j.targets = targets;
-    j.target_bytes = target_bytes;
+    j.tcol = tcol;
+    j.lo = lo;
     j.out = dhidden;
-    j.n = static_cast<uint64_t>(tokens) * dim;
+    j.tokens = pl.tokens;
     j.dim = pl.dim;
     j.splits = pl.splits;
-    j.vocab = pl.sh.vocab;
     if ((e = rr::launch_join(j, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: dhidden");
   }
   return ok();

@@ -95,6 +95,8 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
     pl.xg = take(pl.tokens_pad * row);
     pl.grad = take(static_cast<uint64_t>(pl.tokens_pad) * piece * pl.esz);
     pl.acc = take(static_cast<uint64_t>(pl.splits) * tokens * dim * 4);
+    pl.tcol = take(static_cast<uint64_t>(tokens) * 4);
+    pl.lo = take(static_cast<uint64_t>(tokens) * 4);
     pl.scale = take(4);
   }
   if (pack) {

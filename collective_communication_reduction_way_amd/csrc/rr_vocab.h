@@ -17,6 +17,7 @@
 namespace rr {
 
 constexpr uint32_t kSlot = 64;
+constexpr uint32_t kMasked = 0xFFFFFFFFu;  // "padded column" of a masked token's target
 
 struct VocabShards {
   const void* w[RR_MAX_RANKS];       // row 0 of each shard's [rows, dim] matrix
@@ -48,6 +49,8 @@ struct LogitArgs {
   float* part;            // forward: [tile][tokens][2] maximum and sum
   float* hit;             // forward: the target's logit
   void* grad;             // gradient: [tokens rounded up to kSlot][ld] in the storage type
+  const uint32_t* tcol;   // gradient: the targets' padded columns (kMasked: none)
+  float* lo;              // gradient, 16-bit types: what rounding took from the target's entry
   uint64_t ld;
   uint32_t tokens;
   uint32_t grad_rows;     // gradient: rows of `grad`, zeros from `tokens` on
@@ -81,7 +84,10 @@ struct WeightGradArgs {
   uint64_t ld;
   const void* xg;         // [tokens rounded up to kSlot][xg_stride bytes]
   uint64_t xg_stride;
-  const float* scale;     // device scalar (float16) or NULL
+  const int32_t* scale;   // float16: the device's exponent of the largest loss gradient
+  const uint32_t* tcol;   // as in LogitArgs
+  const float* lo;
+  uint32_t tokens;
   uint32_t rows;          // K: tokens rounded up to kSlot
   uint32_t dim;
   uint32_t c0, c1;
@@ -90,17 +96,18 @@ struct WeightGradArgs {
 
 // Copies rows of `dim` elements into rows of out_stride bytes, zero-filled:
 // the hidden rows (masked rows become zero when targets is given; float16
-// rows are scaled by grad_loss / *scale).
+// rows are scaled by a power of two, see token_exponent).
 struct PackRowsArgs {
+  VocabShards sh;
   const void* x;
   void* out;
   const void* targets;    // NULL: every row counts
   const float* grad_loss; // NULL: no scaling
-  const float* scale;
+  const int32_t* scale;
+  uint32_t* tcol;         // NULL, or the targets' padded columns are written here
   uint64_t out_stride;    // bytes
   uint32_t tokens, rows;  // rows: written rows, zero from `tokens` on
   uint32_t dim;
-  uint32_t vocab;
   int32_t target_bytes;
 };
 
@@ -123,14 +130,14 @@ struct LossArgs {
 };
 
 struct JoinArgs {
+  VocabShards sh;         // the caller's weights
   const float* acc;
   uint64_t split_stride;
-  const float* grad_loss; // float16: row scale grad_loss * 2^-15; else NULL
-  const void* targets;
+  const float* grad_loss; // float16: for the row's scale; else NULL
+  const uint32_t* tcol;
+  const float* lo;        // 16-bit types
   void* out;
-  uint64_t n;             // tokens * dim
-  uint32_t dim, splits, vocab;
-  int32_t target_bytes;
+  uint32_t tokens, dim, splits;
 };
 
 hipError_t launch_logits(const LogitArgs& a, Kind k, VocabTile t, bool grad, hipStream_t s);
@@ -140,7 +147,7 @@ hipError_t launch_pack_rows(const PackRowsArgs& a, Kind k, hipStream_t s);
 hipError_t launch_pack_weight(const PackWeightArgs& a, Kind k, hipStream_t s);
 hipError_t launch_loss(const LossArgs& a, hipStream_t s);
 hipError_t launch_grad_scale(const float* grad_loss, const void* targets, int target_bytes, uint32_t tokens,
-                             uint32_t vocab, float* scale, hipStream_t s);
+                             uint32_t vocab, int32_t* scale, hipStream_t s);
 hipError_t launch_join(const JoinArgs& a, Kind k, hipStream_t s);
 
 // The matrix-product launchers of one element kind (one translation unit each).
@@ -165,7 +172,7 @@ struct VocabPlan {
   uint32_t splits;
   uint32_t tiles;         // forward M tiles over all pieces
   // workspace offsets in bytes
-  uint64_t part, hit, pack_x, pack_w, xg, grad, acc, scale, total;
+  uint64_t part, hit, pack_x, pack_w, xg, grad, acc, tcol, lo, scale, total;
 };
 
 // pack: the inputs are copied into aligned rows first.  The sizes must be valid.

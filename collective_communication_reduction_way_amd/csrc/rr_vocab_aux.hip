@@ -2,15 +2,14 @@
 // products: joining the softmax statistics of the vocabulary's tiles, copying
 // rows into aligned ones, joining split sums.  All are bound by memory and
 // small beside the products.
-#include "rr_device.h"
-#include "rr_vocab.h"
+#include "rr_vocab_device.h"
 
 namespace rr {
 
 namespace {
 
 __device__ __forceinline__ bool counts(const void* targets, int bytes, uint32_t i, uint32_t vocab) {
-  const int64_t y = bytes == 8 ? static_cast<const int64_t*>(targets)[i] : static_cast<const int32_t*>(targets)[i];
+  const int64_t y = target_at(targets, bytes, i);
   return y >= 0 && y < static_cast<int64_t>(vocab);
 }
 
@@ -54,22 +53,22 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a) {
   }
 }
 
-// One workgroup: the largest finite |grad_loss| of the tokens that count (1 if
-// there is none but zeros).
+// One workgroup: the largest exponent of the loss gradients that count.
 __global__ __launch_bounds__(1024) void k_grad_scale(const float* g, const void* targets, int target_bytes,
-                                                     uint32_t tokens, uint32_t vocab, float* scale) {
-  __shared__ float sm[16];
-  float mx = 0.f;
+                                                     uint32_t tokens, uint32_t vocab, int32_t* scale) {
+  __shared__ int sm[16];
+  int top = -150;  // below every float32 exponent
   for (uint32_t i = threadIdx.x; i < tokens; i += 1024) {
-    const float v = fabsf(g[i]);
-    if (v < __builtin_inff() && counts(targets, target_bytes, i, vocab)) mx = fmaxf(mx, v);
+    const float v = g[i];
+    if (v != 0.f && fabsf(v) < __builtin_inff() && counts(targets, target_bytes, i, vocab))
+      top = max(top, token_exponent(v));
   }
-  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = mx;
+  for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sm[i]);
-    *scale = mx > 0.f ? mx : 1.f;
+    for (int i = 1; i < 16; ++i) top = max(top, sm[i]);
+    *scale = top == -150 ? 0 : top;
   }
 }
 
@@ -90,15 +89,18 @@ __global__ __launch_bounds__(256) void k_pack_rows(PackRowsArgs a) {
   using S = typename E::S;
   constexpr uint32_t EPC = 16 / sizeof(S);
   const uint32_t t = blockIdx.x;
-  const bool live = t < a.tokens && (!a.targets || counts(a.targets, a.target_bytes, t, a.vocab));
+  uint32_t col = 0;
+  if (t < a.tokens && a.targets) {
+    col = padded_col(a.sh, target_at(a.targets, a.target_bytes, t));
+    if (a.tcol && threadIdx.x == 0) a.tcol[t] = col;
+  }
+  const bool live = t < a.tokens && col != kMasked;
   float f = 1.f;
-  bool scaled = false;
   if (a.grad_loss && live) {
     const float g = a.grad_loss[t];
-    // float16: g relative to the largest, so that the product stays in the
-    // type's range; equal weights scale by exactly 1 and add no rounding
-    f = fabsf(g) < __builtin_inff() ? g / a.scale[0] : g;
-    scaled = f != 1.f;
+    // a row of g = 0 counts for nothing; one of infinite or NaN g makes the
+    // sums that already at scale 1
+    f = g == 0.f ? 0.f : fabsf(g) < __builtin_inff() ? ldexpf(1.f, token_exponent(g) - a.scale[0]) : 1.f;
   }
   const S* row = static_cast<const S*>(a.x) + static_cast<uint64_t>(t) * a.dim;
   const bool vec = a.dim % EPC == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
@@ -112,7 +114,7 @@ __global__ __launch_bounds__(256) void k_pack_rows(PackRowsArgs a) {
       for (uint32_t j = 0; j < EPC; ++j) v[j] = S(0);
     }
     if constexpr (__is_same(E, EF16)) {
-      if (scaled) {
+      if (f != 1.f) {
 #pragma unroll
         for (uint32_t j = 0; j < EPC; ++j) v[j] = static_cast<S>(f32_to_f16_bits(f16_bits_to_f32(v[j]) * f));
       }
@@ -142,14 +144,26 @@ __global__ __launch_bounds__(256) void k_pack_weight(PackWeightArgs a) {
   }
 }
 
-// dhidden = the sum of the splits' float32 accumulators, rounded once.  A
+// dhidden = the sum of the splits' float32 accumulators, plus what rounding
+// took from the target's entry times the target's weights, rounded once.  A
 // masked token's row is zero whatever the weights hold.
 template <class E>
 __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
   using S = typename E::S;
   const uint32_t t = blockIdx.x;
-  const bool live = counts(a.targets, a.target_bytes, t, a.vocab);
-  const float f = a.grad_loss && live ? a.grad_loss[t] * (1.f / 32768.f) : 1.f;
+  const uint32_t col = a.tcol[t];
+  const bool live = col != kMasked;
+  float f = 1.f, lo = 0.f;
+  const S* w = nullptr;
+  if (live) {
+    if constexpr (__is_same(E, EF16)) f = ldexpf(1.f, token_exponent(a.grad_loss[t]) - 15);
+    if constexpr (sizeof(S) == 2) {
+      lo = a.lo[t];
+      for (int r = 0; r < a.sh.p; ++r)
+        if (col >= a.sh.off[r] && col - a.sh.off[r] < a.sh.rows[r])
+          w = static_cast<const S*>(a.sh.w[r]) + static_cast<uint64_t>(col - a.sh.off[r]) * a.dim;
+    }
+  }
   const uint64_t base = static_cast<uint64_t>(t) * a.dim;
   S* out = static_cast<S*>(a.out) + base;
   for (uint32_t d = threadIdx.x; d < a.dim; d += 256) {
@@ -157,7 +171,8 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
     if (live) {
       v = a.acc[base + d];
       for (uint32_t s = 1; s < a.splits; ++s) v += a.acc[s * a.split_stride + base + d];
-      v *= f;
+      if constexpr (sizeof(S) == 2) v = fmaf(lo, load_one<E>(w + d), v);
+      if constexpr (__is_same(E, EF16)) v *= f;
     }
     store_one<E>(out + d, v);
   }
@@ -172,7 +187,7 @@ hipError_t launch_loss(const LossArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_grad_scale(const float* grad_loss, const void* targets, int target_bytes, uint32_t tokens,
-                             uint32_t vocab, float* scale, hipStream_t s) {
+                             uint32_t vocab, int32_t* scale, hipStream_t s) {
   hipLaunchKernelGGL(k_grad_scale, dim3(1), dim3(1024), 0, s, grad_loss, targets, target_bytes, tokens, vocab, scale);
   return hipGetLastError();
 }
@@ -197,7 +212,7 @@ hipError_t launch_pack_weight(const PackWeightArgs& a, Kind k, hipStream_t s) {
 }
 
 hipError_t launch_join(const JoinArgs& a, Kind k, hipStream_t s) {
-  const dim3 g(static_cast<uint32_t>(a.n / a.dim));
+  const dim3 g(a.tokens);
   if (g.x == 0) return hipSuccess;
   switch (k) {
     case Kind::kF32: hipLaunchKernelGGL(k_join<EF32>, g, dim3(256), 0, s, a); break;

@@ -19,7 +19,7 @@
 #pragma once
 
 #include "rr_device.h"
-#include "rr_vocab.h"
+#include "rr_vocab_device.h"
 
 namespace rr {
 
@@ -328,21 +328,6 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tm, uint32_t tn, u
   n = j / width;
 }
 
-__device__ __forceinline__ int64_t target_at(const void* t, int bytes, uint32_t i) {
-  return bytes == 8 ? static_cast<const int64_t*>(t)[i] : static_cast<const int32_t*>(t)[i];
-}
-
-// The padded column of vocabulary row y, or 0xFFFFFFFF for a masked token (y
-// outside the vocabulary).
-__device__ __forceinline__ uint32_t padded_col(const VocabShards& sh, int64_t y) {
-  if (y < 0 || y >= static_cast<int64_t>(sh.vocab)) return 0xFFFFFFFFu;
-  const uint32_t v = static_cast<uint32_t>(y);
-  uint32_t c = 0;
-  for (int r = 0; r < sh.p; ++r)
-    if (v >= sh.first[r] && v - sh.first[r] < sh.rows[r]) c = sh.off[r] + (v - sh.first[r]);
-  return c;
-}
-
 // ---------------------------------------------------------------------------
 // Logits: M = vocabulary, N = tokens.  A lane of an accumulator holds 4
 // consecutive columns of one token.
@@ -461,17 +446,15 @@ __global__ __launch_bounds__(T::NW * 64) void k_logits(LogitArgs a) {
     for (int n = 0; n < T::NT; ++n) {
       const uint32_t t = t0 + n0 + n * 16 + (lane & 15);
       if (t >= a.grad_rows) continue;
-      uint32_t col = 0xFFFFFFFFu;
+      uint32_t col = kMasked;
       float lse = 0.f, g = 0.f;
       if (t < a.tokens) {
-        col = padded_col(a.sh, target_at(a.targets, a.target_bytes, t));
+        col = a.tcol[t];
         lse = a.lse[t];
         g = a.grad_loss[t];
       }
-      const bool live = col != 0xFFFFFFFFu;
-      // float16 keeps the gradient of the logits free of g and times 2^15, so
-      // that probabilities down to 2^-29 stay normal numbers
-      if constexpr (__is_same(E, EF16)) g = 32768.f;
+      const bool live = col != kMasked;
+      if constexpr (__is_same(E, EF16)) g = ldexpf(g, 15 - token_exponent(g));
       S* out = static_cast<S*>(a.grad) + t * a.ld;
 #pragma unroll
       for (int m = 0; m < T::MT; ++m) {
@@ -482,6 +465,17 @@ __global__ __launch_bounds__(T::NW * 64) void k_logits(LogitArgs a) {
           v[j] = live && (have >> (4 * m + j) & 1) ? pr * g : 0.f;
         }
         const uint32_t c = lc + m * 16 - a.c0;
+        if constexpr (sizeof(S) == 2) {
+          // The target's entry is the row's largest by far; what its rounding
+          // takes goes into the two products on the side (k_join,
+          // k_weight_grad), which leaves the rounding of the outputs the
+          // largest error.
+          const uint32_t j = col - (lc + m * 16);
+          if (live && j < 4) {
+            const float x = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
+            a.lo[t] = x - half_to_f32<E>(f32_to_half<E>(x));
+          }
+        }
         if (c < a.c1 - a.c0) {
           if constexpr (sizeof(S) == 4) {
             *reinterpret_cast<f32x4_t*>(out + c) = f32x4_t{v[0], v[1], v[2], v[3]};
@@ -587,8 +581,77 @@ __global__ __launch_bounds__(T::NW * 64) void k_weight_grad(WeightGradArgs a) {
       },
       [&](const char* t, int m, int s) { return frag_ks<E, T::BM>(t, m0 + m * 16, s, lane); },
       [&](const char* t, int n, int s) { return frag_ks<E, T::BN>(t, n0 + n * 16, s, lane); });
+  if constexpr (esz == 2) {
+    // What rounding took from the targets' entries: the tokens whose target
+    // lies in this tile (few: the whole vocabulary shares the tokens) are
+    // listed in order and added as further K steps of 64.
+    __shared__ uint32_t list[64 + T::NW * 64];
+    __shared__ uint32_t found[T::NW];
+    const uint32_t first = a.c0 + v0;
+    uint32_t have = 0;
+    const auto add = [&](uint32_t n) {
+#pragma unroll
+      for (int q = 0; q < KsLoader<E, T::BM, T::NW>::NQ; ++q) {
+        const uint32_t o = (wave + q * T::NW) * 1024 + lane * 16;
+        const uint32_t k = o / (T::BM * esz);
+        const uint32_t c = ks_chunk<E>(k, (o % (T::BM * esz)) / 16) * 16;
+        const bool in = k < n && c < a.xg_stride - static_cast<uint64_t>(d0) * esz;
+        load_to_lds(in ? static_cast<const char*>(a.xg) + list[k] * a.xg_stride + static_cast<uint64_t>(d0) * esz + c
+                       : reinterpret_cast<const char*>(vocab_zero),
+                    lds + o - lane * 16);
+      }
+      for (uint32_t i = threadIdx.x; i < T::BBYTES / 16; i += T::NW * 64)
+        *reinterpret_cast<u32x4*>(lds + T::ABYTES + i * 16) = u32x4{0, 0, 0, 0};
+      __syncthreads();
+      if (threadIdx.x < n) {
+        const uint32_t k = threadIdx.x, t = list[k], c = a.tcol[t] - first;
+        const uint32_t at = k * (T::BN * esz) + (((c >> 4) ^ ks_swizzle<E>(k)) << 5) + (c & 15u) * 2;
+        *reinterpret_cast<S*>(lds + T::ABYTES + at) = static_cast<S>(f32_to_half<E>(a.lo[t]));
+      }
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Frag<E> fa[T::MT], fb[T::NT];
+#pragma unroll
+        for (int m = 0; m < T::MT; ++m) fa[m] = frag_ks<E, T::BM>(lds, m0 + m * 16, s, lane);
+#pragma unroll
+        for (int n2 = 0; n2 < T::NT; ++n2) fb[n2] = frag_ks<E, T::BN>(lds + T::ABYTES, n0 + n2 * 16, s, lane);
+#pragma unroll
+        for (int m = 0; m < T::MT; ++m)
+#pragma unroll
+          for (int n2 = 0; n2 < T::NT; ++n2) acc[m][n2] = mma<E>(fa[m], fb[n2], acc[m][n2]);
+      }
+      __syncthreads();
+    };
+    for (uint32_t b = 0; b < a.tokens; b += T::NW * 64) {
+      const uint32_t t = b + threadIdx.x;
+      const bool in = t < a.tokens && a.tcol[t] - first < T::BN;  // kMasked - first is out of range
+      const uint64_t mask = __ballot(in);
+      if (lane == 0) found[wave] = __popcll(mask);
+      __syncthreads();
+      uint32_t at = have, total = have;
+#pragma unroll
+      for (int w = 0; w < T::NW; ++w) {
+        if (w < wave) at += found[w];
+        total += found[w];
+      }
+      if (in) list[at + __popcll(mask & ((1ull << lane) - 1))] = t;
+      have = total;
+      __syncthreads();
+      while (have >= 64) {
+        add(64);
+        const uint32_t left = have - 64;  // at most NW * 64 - 1
+        const uint32_t v = threadIdx.x < left ? list[64 + threadIdx.x] : 0;
+        __syncthreads();
+        if (threadIdx.x < left) list[threadIdx.x] = v;
+        __syncthreads();
+        have = left;
+      }
+    }
+    if (have > 0) add(have);
+  }
   float scale = 1.f;
-  if constexpr (__is_same(E, EF16)) scale = a.scale[0] * (1.f / 32768.f);
+  if constexpr (__is_same(E, EF16)) scale = ldexpf(1.f, a.scale[0] - 15);
 #pragma unroll
   for (int n = 0; n < T::NT; ++n) {
     const uint32_t c = a.c0 + v0 + n0 + n * 16 + (lane & 15);

@@ -501,9 +501,9 @@ rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weight
  *   dhidden: [tokens, dim], or NULL; dweights: p matrices shaped as weights, or
  *     NULL; not both NULL.  With tokens == 0 dweights is filled with zeros.
  * Arithmetic: the logits are computed again; g is rounded once to the storage
- * type (float16: as a probability times 2^15, and the hidden rows are scaled by
- * grad_loss / max |grad_loss| in float16 for dweights), the products are summed
- * in float32 and rounded once.  The same inputs give the same bits every time.
+ * type (float16: scaled by a power of two per token), except that the target's
+ * entry keeps twice the type's digits; the products are summed in float32 and
+ * rounded once.  The same inputs give the same bits every time.
  */
 rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* weights, const void* targets,
                                         int target_bytes, const float* lse, const float* grad_loss, void* dhidden,

@@ -8,9 +8,11 @@ float32 sum, rounded or truncated):
   lse: |d lse| <= Z + 16 f (log V + |lse| + 4) =: L -- each exponential is off
     by (|argument| + 4) f, weighted by its probability, and the statistics are
     merged a few times; the loss adds one logit and a rounding;
-  gradient of a logit: g (p (Z + L + 4 f) + u |p - onehot|), then sums over V (or
-    T) terms: (terms + 2) f of the sum of the magnitudes, and u of the result;
-    float16 adds u for the scaled hidden rows and its subnormal steps.
+  gradient of a logit: g (p (Z + L + 4 f) + u p), the target's entry u^2 instead
+    of u, then sums over V (or T) terms: (terms + 4) f of the sum of the
+    magnitudes, and u of the result; float16 adds its subnormal steps: 2^-24 of
+    an entry kept at 2^15, 2^-24 of a hidden value scaled by g over the largest
+    g (to a power of two), 2^-24 of an output.
 """
 
 import numpy as np
@@ -75,14 +77,14 @@ def bounds(h, w, t, g, dtype):
     hot[np.arange(T)[live], t[live]] = 1
     # an fp16 gradient entry of a logit has steps of 2^-24 at 2^15 times its size
     tiny = 2.0 ** -39 if dtype == "float16" else 0.0
-    dG = ga[:, None] * (P * (Z + L + 4 * F)[:, None] + 2 * u * np.abs(P - hot) + tiny)
+    dG = ga[:, None] * (P * (Z + L + 4 * F)[:, None] + np.where(hot > 0, u * u, u) * np.abs(P - hot) + 2 * F * P + tiny)
     G = ga[:, None] * np.abs(P - hot)
     out_tiny = 2.0 ** -24 if dtype == "float16" else 0.0
-    th = dG @ np.abs(w) + (V + 2) * F * (G @ np.abs(w)) + u * np.abs(dh) + out_tiny
+    th = dG @ np.abs(w) + (V + 4) * F * (G @ np.abs(w)) + u * np.abs(dh) + out_tiny
     hz = np.where(live[:, None], np.abs(h), 0.0)
-    xtra = (u * (G.T @ hz) + 2.0 ** -25 * ga.max(initial=0.0) * np.abs(P - hot).T @ live[:, None]
+    xtra = (2.0 ** -23 * ga.max(initial=0.0) * np.abs(P - hot).T @ live[:, None].astype(np.float64)
             if dtype == "float16" else 0.0)
-    tw = dG.T @ hz + (T + 2) * F * (G.T @ hz) + u * np.abs(dw) + out_tiny + xtra
+    tw = dG.T @ hz + (T + 4) * F * (G.T @ hz) + u * np.abs(dw) + out_tiny + xtra
     return (loss, lse, dh, dw), (tl, L, th, tw)
 
 
@@ -342,3 +344,17 @@ def test_training_step_end_to_end(rr):
     keep = torch.from_numpy(TR.dropout_keep(T * d, 0.1, 5, 6)).cuda()
     want = torch.where(keep, dy.reshape(-1).float() * np.float32(1 / 0.9), torch.zeros((), device="cuda")).bfloat16()
     assert all(torch.equal(dparts[r], want) for r in range(p))
+
+
+def test_many_tokens_of_one_target(rr):
+    """More tokens of one target than one K step holds, and targets at the ends of shards and slots."""
+    p, T, d, V = 3, 900, 136, 1000
+    h, w, t, g = inputs(13, p, T, d, V, "bfloat16", masked=0.05)
+    t[(t >= 0) & (torch.arange(T, device="cuda") % 3 > 0)] = 333
+    t[0], t[1], t[2], t[3] = 0, 332, 666, 999
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    want, tol = bounds(h, w, t, g, "bfloat16")
+    check(loss, want[0], tol[0], "loss")
+    check(dh, want[2], tol[2], "dhidden")
+    check(torch.cat(dw), want[3], tol[3], "dweights")
