@@ -1615,6 +1615,12 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   h.tiles_m = tiles_over(dim, rr::tile_m(pl.hidden_tile));
   h.tiles_n = tiles_over(tokens, rr::tile_n(pl.hidden_tile));
   h.splits = pl.splits;
+  // dhidden straight from the product where that is all of the sum
+  const bool direct = dhidden && !pack && pl.pieces == 1 && pl.splits == 1 && aligned16(dhidden);
+  h.out = direct ? dhidden : nullptr;
+  h.tcol = tcol;
+  h.lo = lo;
+  h.grad_loss = grad_loss;
   rr::WeightGradArgs w;
   memset(&w, 0, sizeof(w));
   w.grad = a.grad;
@@ -1627,8 +1633,12 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   w.rows = pl.tokens_pad;
   w.dim = pl.dim;
   w.tiles_m = tiles_over(dim, rr::tile_m(pl.weight_tile));
+  w.vec = (dim * esz) % 16 == 0 ? 1 : 0;
   if (dweights)
-    for (int r = 0; r < p; ++r) w.dw[r] = dweights[r];
+    for (int r = 0; r < p; ++r) {
+      w.dw[r] = dweights[r];
+      if (pl.sh.rows[r] && !aligned16(dweights[r])) w.vec = 0;
+    }
   for (uint32_t c0 = 0; c0 < pl.sh.off[p]; c0 += pl.piece) {
     const uint32_t c1 = std::min(pl.sh.off[p], c0 + pl.piece);
     if ((e = vocab_piece(pl, sh, pack, k, c0, c1, ws, a.sh, s)) != hipSuccess)
@@ -1652,7 +1662,7 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
         return hip_fail(e, "vocab_cross_entropy_grad: dweights");
     }
   }
-  if (dhidden && tokens > 0) {
+  if (dhidden && !direct) {
     rr::JoinArgs j;
     j.sh = sh;
     j.acc = h.acc;

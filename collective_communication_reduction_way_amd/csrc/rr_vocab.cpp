@@ -13,7 +13,7 @@ namespace {
 
 // The gradient of the logits of one piece of the vocabulary is kept at a time
 // (storage type): a piece is as wide as fits here.
-constexpr uint64_t kGradBytes = 256ull << 20;
+constexpr uint64_t kGradBytes = 1ull << 30;
 // Copied weight rows of one piece (inputs whose rows are not 16-byte aligned).
 constexpr uint64_t kPackBytes = 64ull << 20;
 constexpr uint32_t kPieceUnit = 256;
@@ -48,7 +48,8 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
   uint64_t most = off;
   if (grad && pl.tokens_pad) most = std::min<uint64_t>(most, kGradBytes / (static_cast<uint64_t>(pl.tokens_pad) * pl.esz));
   if (pack) most = std::min<uint64_t>(most, kPackBytes / row);
-  // a grid of at most 2^22 workgroups
+  // a grid of at most 2^22 workgroups, and 32-bit offsets within a tile
+  most = std::min<uint64_t>(most, 1u << 20);
   most = std::min<uint64_t>(most, (1ull << 22) / std::max(1u, ceil_div(tokens, 256)) * 256);
   most = std::max<uint64_t>(most / kPieceUnit * kPieceUnit, kPieceUnit);
   pl.pieces = ceil_div(off, most);

@@ -74,6 +74,10 @@ struct HiddenGradArgs {
   uint32_t c0, c1;
   uint32_t tiles_m, tiles_n, splits;
   int32_t add;            // 1: add to what the accumulators hold (pieces after the first)
+  void* out;              // dhidden, where one product is all of it (rows 16-byte aligned); else NULL
+  const uint32_t* tcol;   // with out: as in LogitArgs
+  const float* lo;
+  const float* grad_loss;
 };
 
 // dweights of a piece = grad^T * xg (xg: the hidden rows that count).
@@ -92,6 +96,7 @@ struct WeightGradArgs {
   uint32_t dim;
   uint32_t c0, c1;
   uint32_t tiles_m, tiles_n;
+  int32_t vec;            // 1: rows of dweights are 16-byte aligned
 };
 
 // Copies rows of `dim` elements into rows of out_stride bytes, zero-filled:

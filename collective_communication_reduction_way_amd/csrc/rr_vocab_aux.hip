@@ -144,38 +144,66 @@ __global__ __launch_bounds__(256) void k_pack_weight(PackWeightArgs a) {
   }
 }
 
-// dhidden = the sum of the splits' float32 accumulators, plus what rounding
-// took from the target's entry times the target's weights, rounded once.  A
-// masked token's row is zero whatever the weights hold.
-template <class E>
+// dhidden = the sum of the splits' float32 accumulators, finished and rounded
+// once.  A workgroup takes 1024 columns of a row, or 256 where there are many
+// splits: then 4 threads share a column's splits, so that a few tokens' few
+// columns are not one long chain of loads.
+template <class E, int G, int V>
 __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
   using S = typename E::S;
+  constexpr uint32_t kCols = 256 / G * V;
+  __shared__ float part[G][kCols];
   const uint32_t t = blockIdx.x;
-  const uint32_t col = a.tcol[t];
-  const bool live = col != kMasked;
-  float f = 1.f, lo = 0.f;
-  const S* w = nullptr;
-  if (live) {
-    if constexpr (__is_same(E, EF16)) f = ldexpf(1.f, token_exponent(a.grad_loss[t]) - 15);
-    if constexpr (sizeof(S) == 2) {
-      lo = a.lo[t];
-      for (int r = 0; r < a.sh.p; ++r)
-        if (col >= a.sh.off[r] && col - a.sh.off[r] < a.sh.rows[r])
-          w = static_cast<const S*>(a.sh.w[r]) + static_cast<uint64_t>(col - a.sh.off[r]) * a.dim;
+  const uint32_t c = threadIdx.x % (256 / G), g = threadIdx.x / (256 / G);
+  const uint32_t d = blockIdx.y * kCols + c * V;
+  const HiddenRow<E> h(a.sh, a.tcol, a.lo, a.grad_loss, t, a.tokens, a.dim);
+  const uint64_t at = static_cast<uint64_t>(t) * a.dim + d;
+  float v[V] = {};
+  if (h.live && d < a.dim) {
+    const float* p = a.acc + at;
+    const uint32_t lo = a.splits * g / G, hi = a.splits * (g + 1) / G;
+#pragma unroll 8
+    for (uint32_t s = lo; s < hi; ++s) {
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + s * a.split_stride);
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
+      } else {
+        v[0] += p[s * a.split_stride];
+      }
     }
   }
-  const uint64_t base = static_cast<uint64_t>(t) * a.dim;
-  S* out = static_cast<S*>(a.out) + base;
-  for (uint32_t d = threadIdx.x; d < a.dim; d += 256) {
-    float v = 0.f;
-    if (live) {
-      v = a.acc[base + d];
-      for (uint32_t s = 1; s < a.splits; ++s) v += a.acc[s * a.split_stride + base + d];
-      if constexpr (sizeof(S) == 2) v = fmaf(lo, load_one<E>(w + d), v);
-      if constexpr (__is_same(E, EF16)) v *= f;
-    }
-    store_one<E>(out + d, v);
+  if constexpr (G > 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) part[g][c * V + j] = v[j];
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int q = 1; q < G; ++q)
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] += part[q][c * V + j];
   }
+  S* out = static_cast<S*>(a.out) + at;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (d + j >= a.dim) break;
+    float w = 0.f;
+    if constexpr (sizeof(S) == 2) w = h.live ? load_one<E>(h.w + d + j) : 0.f;
+    store_one<E>(out + j, h.live ? h.finish(v[j], w) : 0.f);
+  }
+}
+
+template <class E>
+void run_join(const JoinArgs& a, hipStream_t s) {
+  const bool many = a.splits >= 8, vec = a.dim % 4 == 0;
+  const uint32_t cols = (many ? 64 : 256) * (vec ? 4 : 1);
+  const dim3 g(a.tokens, (a.dim + cols - 1) / cols);
+  if (many && vec) hipLaunchKernelGGL((k_join<E, 4, 4>), g, dim3(256), 0, s, a);
+  else if (many) hipLaunchKernelGGL((k_join<E, 4, 1>), g, dim3(256), 0, s, a);
+  else if (vec) hipLaunchKernelGGL((k_join<E, 1, 4>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_join<E, 1, 1>), g, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -212,12 +240,11 @@ hipError_t launch_pack_weight(const PackWeightArgs& a, Kind k, hipStream_t s) {
 }
 
 hipError_t launch_join(const JoinArgs& a, Kind k, hipStream_t s) {
-  const dim3 g(a.tokens);
-  if (g.x == 0) return hipSuccess;
+  if (a.tokens == 0) return hipSuccess;
   switch (k) {
-    case Kind::kF32: hipLaunchKernelGGL(k_join<EF32>, g, dim3(256), 0, s, a); break;
-    case Kind::kBF16: hipLaunchKernelGGL(k_join<EBF16>, g, dim3(256), 0, s, a); break;
-    default: hipLaunchKernelGGL(k_join<EF16>, g, dim3(256), 0, s, a); break;
+    case Kind::kF32: run_join<EF32>(a, s); break;
+    case Kind::kBF16: run_join<EBF16>(a, s); break;
+    default: run_join<EF16>(a, s); break;
   }
   return hipGetLastError();
 }

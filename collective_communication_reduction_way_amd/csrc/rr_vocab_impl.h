@@ -28,21 +28,45 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 #define RR_LDS __attribute__((address_space(3)))
 #define RR_GLB __attribute__((address_space(1)))
 
-// What out-of-range chunks read.
-static __device__ __attribute__((aligned(16))) uint32_t vocab_zero[4];
+// A stretch of memory that a wavefront loads from: reads at or past `bytes` give
+// zeros, which is how rows and columns that do not exist are read.
+struct Span {
+  const char* base;  // the same in every lane
+  uint32_t bytes;
+};
+constexpr uint32_t kNoOffset = 0xFFFFFFF0u;  // past the end of every span
+
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const char*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 // 16 bytes a lane from memory straight into LDS; `lds` is the wavefront's base
-// and lane l's chunk lands at lds + 16 l.
-__device__ __forceinline__ void load_to_lds(const void* g, char* lds) {
-  __builtin_amdgcn_global_load_lds(reinterpret_cast<const RR_GLB void*>(reinterpret_cast<uintptr_t>(g)),
-                                   reinterpret_cast<RR_LDS void*>(static_cast<uint32_t>(
-                                       reinterpret_cast<uintptr_t>(lds))),
-                                   16, 0, 0);
+// and lane l's chunk lands at lds + 16 l.  The instruction is written out
+// because for the builtin the compiler waits for all loads in flight before the
+// next transposing LDS read, whatever it reads.  Nothing comes back in
+// registers; wait_for_loads() stands before the barrier after which the LDS is
+// read.  (One wait state is due between the write of M0 and its use.)
+__device__ __forceinline__ void load_to_lds(const Span& m, uint32_t offset, char* lds) {
+  const uint64_t base = reinterpret_cast<uint64_t>(uniform(m.base));
+  const u32x4 r = {static_cast<uint32_t>(base), static_cast<uint32_t>(base >> 32) & 0xFFFFu,
+                   static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(m.bytes)), 0x00027000u};
+  const uint32_t to = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((RR_LDS char*)lds)));
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // M0 is reserved: nothing of the compiler's lives in it
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(r)
+               : "m0");
+#pragma clang diagnostic pop
 }
+__device__ __forceinline__ void wait_for_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 template <class E>
 struct Frag {
@@ -52,21 +76,22 @@ struct Frag {
   u32x4 v;
 };
 
-// One step of a 16 x 16 product: 32 values of k in 16-bit types, 16 in float32
-// (there lane group g holds k = 4g .. 4g+3, and the j-th instruction multiplies
-// the four values k = 4g + j).
+// A 32 x 32 product over a quarter of a step: 16 values of k in 16-bit types (lane
+// half h holds k = 8h .. 8h+7), 8 in float32 (half h holds k = 4h .. 4h+3, and the
+// j-th instruction multiplies k = j and 4 + j).  Lane l of the result holds column
+// l mod 32 and, in register 4i + j, row 8i + 4 (l / 32) + j.
 template <class E>
-__device__ __forceinline__ f32x4_t mma(const Frag<E>& a, const Frag<E>& b, f32x4_t c) {
+__device__ __forceinline__ f32x16_t mma(const Frag<E>& a, const Frag<E>& b, f32x16_t c) {
   if constexpr (__is_same(E, EBF16)) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v),
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a.v),
                                                    __builtin_bit_cast(bf16x8_t, b.v), c, 0, 0, 0);
   } else if constexpr (__is_same(E, EF16)) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a.v),
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a.v),
                                                   __builtin_bit_cast(f16x8_t, b.v), c, 0, 0, 0);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.v[j]), __uint_as_float(b.v[j]), c, 0, 0, 0);
+      c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a.v[j]), __uint_as_float(b.v[j]), c, 0, 0, 0);
     return c;
   }
 }
@@ -74,46 +99,47 @@ __device__ __forceinline__ f32x4_t mma(const Frag<E>& a, const Frag<E>& b, f32x4
 // ---------------------------------------------------------------------------
 // LDS layouts.
 
-// KS: the permutation of a row's units of 16 elements.  16-bit: lanes 0-31 of
-// a transposing read touch rows 8g + (0..3), g = 0, 1, of one unit.  float32: a
-// read touches rows 4g, g = 0..3, of one unit.
+// KS: the permutation of a row's units of 16 elements, chosen so that the rows
+// and units that half a wavefront reads at once lie in different banks:
+// 16-bit, rows k .. k+3 of two adjacent units (32 bytes each); float32, rows k
+// and k+4 of two adjacent units (64 bytes each).
 template <class E>
 __device__ __forceinline__ uint32_t ks_swizzle(uint32_t k) {
   if constexpr (sizeof(typename E::S) == 2) {
-    return (k & 3u) | ((k >> 1) & 4u);
+    return (k & 3u) << 1;
   } else {
-    return (k >> 2) & 3u;
+    return (k >> 1) & 2u;
   }
 }
 
-// Fragment of rows r0 .. r0+15 of a KC tile, k substep s (0 or 1).
+// Fragment of rows r0 .. r0+31 of a KC tile, quarter s of the step.
 template <class E>
 __device__ __forceinline__ Frag<E> frag_kc(const char* tile, int r0, int s, int lane) {
-  const int row = r0 + (lane & 15);
-  const int chunk = (s * 4 + (lane >> 4)) ^ (lane & 7);
+  const int row = r0 + (lane & 31);
+  const int chunk = (s * 2 + (lane >> 5)) ^ ((lane >> 1) & 7);
   Frag<E> f;
   f.v = *reinterpret_cast<const u32x4*>(tile + row * 128 + chunk * 16);
   return f;
 }
 
-// Fragment of columns c0 .. c0+15 of a KS tile of R columns.
+// Fragment of columns c0 .. c0+31 of a KS tile of R columns.
 template <class E, int R>
 __device__ __forceinline__ Frag<E> frag_ks(const char* tile, int c0, int s, int lane) {
   Frag<E> f;
+  const uint32_t u = static_cast<uint32_t>(c0 >> 4) + ((lane >> 4) & 1);
   if constexpr (sizeof(typename E::S) == 2) {
-    const int k = s * 32 + (lane >> 4) * 8 + ((lane >> 2) & 3);
-    const uint32_t unit = static_cast<uint32_t>(c0 >> 4) ^ ks_swizzle<E>(k);
-    const char* q = tile + k * (R * 2) + unit * 32 + (lane & 3) * 8;
+    // 16 lanes read 4 rows of 16 columns and get a column of 4 rows each
+    const int k = s * 16 + (lane >> 5) * 8 + ((lane >> 2) & 3);
+    const char* q = tile + k * (R * 2) + (u ^ ks_swizzle<E>(k)) * 32 + (lane & 3) * 8;
     const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        reinterpret_cast<RR_LDS s16x4_t*>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q))));
+        (RR_LDS s16x4_t*)(q));
     const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        reinterpret_cast<RR_LDS s16x4_t*>(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(q + 4 * R * 2))));
+        (RR_LDS s16x4_t*)(q + 4 * R * 2));
     const s16x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     f.v = __builtin_bit_cast(u32x4, v);
   } else {
-    const int k = s * 16 + (lane >> 4) * 4;
-    const uint32_t unit = static_cast<uint32_t>(c0 >> 4) ^ ks_swizzle<E>(k);
-    const char* q = tile + k * (R * 4) + unit * 64 + (lane & 15) * 4;
+    const int k = s * 8 + (lane >> 5) * 4;
+    const char* q = tile + k * (R * 4) + (u ^ ks_swizzle<E>(k)) * 64 + (lane & 15) * 4;
 #pragma unroll
     for (int j = 0; j < 4; ++j) f.v[j] = *reinterpret_cast<const uint32_t*>(q + j * (R * 4));
   }
@@ -121,7 +147,7 @@ __device__ __forceinline__ Frag<E> frag_ks(const char* tile, int c0, int s, int 
 }
 
 // The global 16-byte chunk that belongs at LDS chunk `pos` of a row.
-__device__ __forceinline__ uint32_t kc_chunk(uint32_t row, uint32_t pos) { return pos ^ (row & 7u); }
+__device__ __forceinline__ uint32_t kc_chunk(uint32_t row, uint32_t pos) { return pos ^ ((row >> 1) & 7u); }
 template <class E>
 __device__ __forceinline__ uint32_t ks_chunk(uint32_t k, uint32_t pos) {
   if constexpr (sizeof(typename E::S) == 2) {
@@ -133,137 +159,187 @@ __device__ __forceinline__ uint32_t ks_chunk(uint32_t k, uint32_t pos) {
 
 // ---------------------------------------------------------------------------
 // Loaders.  A tile of R rows or columns is R*128 bytes = R/8 wavefront loads;
-// wavefront w of NW issues loads w, w + NW, ...
+// wavefront w of the 4 issues loads w, w + 4, ...  Offsets within a tile are 32
+// bits (a tile's 256 rows span less than 2^31 bytes), the bases advance.
+constexpr int kWaves = 4;
 
-// KC: row pointers fixed for the whole product; k advances 128 bytes a step.
-template <int R, int NW>
+// KC over rows at a constant stride: rows row0 .. of a matrix of `rows` rows.
+template <int R>
 struct KcLoader {
-  static constexpr int NQ = R / 8 / NW;
-  const char* ptr[NQ];   // row + this lane's chunk, or the zero chunk
-  uint32_t left;         // bytes of the row from the lane's chunk on (0 for a row out of range: see step)
-  uint32_t in_row;       // bit q: row q is in range
-  uint32_t base;         // LDS offset of the wavefront's first load
+  static constexpr int NQ = R / 8 / kWaves;
+  uint32_t off[NQ];
+  uint32_t left;  // bytes of a row from the lane's chunk on
+  Span m;
+  int wave;
 
-  template <class ROW>
-  __device__ __forceinline__ void init(ROW row_ptr, uint32_t kbytes, int wave, int lane) {
-    in_row = 0;
-    const uint32_t chunk = kc_chunk(lane >> 3, lane & 7);
-    left = kbytes > chunk * 16 ? kbytes - chunk * 16 : 0;
-    base = wave * 1024;
+  __device__ __forceinline__ void init(const void* src, uint64_t stride, uint32_t row0, uint32_t rows, uint32_t kbytes,
+                                       uint32_t kt, int wave_, int lane) {
+    wave = wave_;
+    const uint32_t chunk = kc_chunk(wave * 8 + (lane >> 3), lane & 7) * 16;
+    const uint32_t skip = kt * 128;
+    left = kbytes > chunk + skip ? kbytes - chunk - skip : 0;
+    const uint32_t n = row0 < rows ? (rows - row0 < R ? rows - row0 : R) : 0;
+    m.base = uniform(static_cast<const char*>(src) + row0 * stride + skip);
+    m.bytes = n ? n * static_cast<uint32_t>(stride) - skip : 0;
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const char* r = row_ptr((wave + q * NW) * 8 + (lane >> 3));
-      if (r) {
-        ptr[q] = r + chunk * 16;
-        in_row |= 1u << q;
-      } else {
-        ptr[q] = reinterpret_cast<const char*>(vocab_zero);
+    for (int q = 0; q < NQ; ++q)
+      off[q] = ((wave + q * kWaves) * 8 + (lane >> 3)) * static_cast<uint32_t>(stride) + chunk;
+  }
+  __device__ __forceinline__ void prepare() {}
+  // Load q of the next step (zeros after the last one).
+  __device__ __forceinline__ void load(int q, char* lds) {
+    load_to_lds(m, left ? off[q] : kNoOffset, lds + (wave + q * kWaves) * 1024);
+  }
+  __device__ __forceinline__ void advance() {
+    m.base += 128;
+    m.bytes = m.bytes > 128 ? m.bytes - 128 : 0;
+    left = left > 128 ? left - 128 : 0;
+  }
+};
+
+// KC over the padded vocabulary: a slot of kSlot columns is kSlot rows of one
+// shard, and two of a wavefront's loads.
+template <int R>
+struct KcShardLoader {
+  static constexpr int NS = R / kSlot, NQ = 2 * NS;
+  static_assert(kSlot == 2 * 8 * kWaves, "two loads a slot");
+  uint32_t off[2];
+  uint32_t left;
+  Span m[NS];
+  int wave;
+
+  __device__ __forceinline__ void init(const VocabShards& sh, uint64_t stride, uint32_t col, uint32_t col_end,
+                                       uint32_t kbytes, int wave_, int lane) {
+    wave = wave_;
+    const uint32_t chunk = kc_chunk(wave * 8 + (lane >> 3), lane & 7) * 16;
+    left = kbytes > chunk ? kbytes - chunk : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) off[i] = ((wave + i * kWaves) * 8 + (lane >> 3)) * static_cast<uint32_t>(stride) + chunk;
+    int r = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const uint32_t c = col + s * kSlot;
+      m[s] = Span{nullptr, 0};
+      if (c < col_end) {
+        while (c >= sh.off[r + 1]) ++r;  // c < off[p]: ends at the shard that holds c
+        const uint32_t local = c - sh.off[r];
+        const uint32_t n = sh.rows[r] - local < kSlot ? sh.rows[r] - local : kSlot;
+        m[s].base = uniform(static_cast<const char*>(sh.w[r]) + local * stride);
+        m[s].bytes = n * static_cast<uint32_t>(stride);
       }
     }
   }
-  // Skip to k step kt.
-  __device__ __forceinline__ void seek(uint32_t kt) {
-    const uint32_t b = kt * 128;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-      if (in_row >> q & 1) ptr[q] += b;
-    left = left > b ? left - b : 0;
+  __device__ __forceinline__ void prepare() {}
+  __device__ __forceinline__ void load(int q, char* lds) {
+    load_to_lds(m[q / 2], left ? off[q % 2] : kNoOffset, lds + (wave + q * kWaves) * 1024);
   }
-  // Issue the loads of the next step.
-  __device__ __forceinline__ void step(char* lds) {
+  __device__ __forceinline__ void advance() {
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const char* g = left ? ptr[q] : reinterpret_cast<const char*>(vocab_zero);
-      load_to_lds(g, lds + base + q * NW * 1024);
-      if (in_row >> q & 1) ptr[q] += 128;
+    for (int s = 0; s < NS; ++s) {
+      m[s].base += 128;
+      m[s].bytes = m[s].bytes > 128 ? m[s].bytes - 128 : 0;
     }
     left = left > 128 ? left - 128 : 0;
   }
 };
 
-// KS with rows at a constant stride: row k of step kt is base + (kt*BK + k)*stride.
-// `cols` is the number of valid bytes of a row from the tile's first column on.
-template <class E, int R, int NW>
-struct KsLoader {
-  static constexpr int NQ = R / 8 / NW;
+// Offsets of a KS tile's loads: `cols` valid bytes of a row from the tile's
+// first column on.
+template <class E, int R>
+struct KsOffsets {
+  static constexpr int NQ = R / 8 / kWaves;
   static constexpr int RB = R * static_cast<int>(sizeof(typename E::S));
-  const char* ptr[NQ];
-  uint64_t step_bytes;
-  uint32_t in_cols;
-  uint32_t base;
-
-  __device__ __forceinline__ void init(const void* src, uint64_t stride, uint64_t cols, uint32_t kt, int wave,
-                                       int lane) {
-    step_bytes = stride * Frag<E>::kBK;
-    in_cols = 0;
-    base = wave * 1024;
+  uint32_t off[NQ];
+  __device__ __forceinline__ void init(uint32_t stride, uint64_t cols, int wave, int lane) {
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      const uint32_t o = (wave + q * NW) * 1024 + lane * 16;
+      const uint32_t o = (wave + q * kWaves) * 1024 + lane * 16;
       const uint32_t k = o / RB;
       const uint32_t c = ks_chunk<E>(k, (o % RB) / 16) * 16;
-      if (c < cols) {
-        ptr[q] = static_cast<const char*>(src) + kt * step_bytes + k * stride + c;
-        in_cols |= 1u << q;
-      } else {
-        ptr[q] = reinterpret_cast<const char*>(vocab_zero);
-      }
-    }
-  }
-  __device__ __forceinline__ void step(char* lds) {
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      load_to_lds(ptr[q], lds + base + q * NW * 1024);
-      if (in_cols >> q & 1) ptr[q] += step_bytes;
+      off[q] = c < cols ? k * stride + c : kNoOffset;
     }
   }
 };
 
-// KS over the padded vocabulary: a step's rows are rows of one shard, rows
-// past its end read zeros.
-template <class E, int R, int NW>
-struct KsShardLoader {
-  static constexpr int NQ = R / 8 / NW;
-  static constexpr int RB = R * static_cast<int>(sizeof(typename E::S));
-  uint64_t rel[NQ];      // byte offset of the lane's chunk from the step's first row and the tile's first column
-  uint32_t krow[NQ];
-  uint32_t in_cols;
-  uint32_t base;
-  uint64_t stride;
-  uint64_t col0;
-  uint32_t c;            // padded column of the next step
-  int r;                 // its shard
+// KS with rows at a constant stride, all of them there.
+template <class E, int R>
+struct KsLoader {
+  static constexpr int NQ = KsOffsets<E, R>::NQ;
+  KsOffsets<E, R> o;
+  Span m;
+  uint64_t step_bytes;
+  uint32_t steps;  // that are left
+  int wave;
 
-  __device__ __forceinline__ void init(const VocabShards& sh, uint64_t stride_, uint64_t col0_, uint64_t cols,
-                                       uint32_t c_, int wave, int lane) {
-    in_cols = 0;
-    base = wave * 1024;
+  __device__ __forceinline__ void init(const char* src, uint64_t stride, uint64_t cols, uint32_t steps_, int wave_,
+                                       int lane) {
+    wave = wave_;
+    steps = steps_;
+    o.init(static_cast<uint32_t>(stride), cols, wave, lane);
+    step_bytes = stride * Frag<E>::kBK;
+    m.base = uniform(src);
+    // the step's rows, up to the last byte of the last one that belongs to the tile's columns
+    m.bytes = static_cast<uint32_t>(step_bytes - stride + (cols < KsOffsets<E, R>::RB ? cols : KsOffsets<E, R>::RB));
+  }
+  __device__ __forceinline__ void prepare() {}
+  __device__ __forceinline__ void load(int q, char* lds) {
+    load_to_lds(Span{m.base, steps ? m.bytes : 0}, o.off[q], lds + (wave + q * kWaves) * 1024);
+  }
+  __device__ __forceinline__ void advance() {
+    m.base += step_bytes;
+    steps -= steps ? 1 : 0;
+  }
+};
+
+// KS over the padded vocabulary, columns [c, end): a step's rows are rows of
+// one shard, rows past its end read zeros.
+template <class E, int R>
+struct KsShardLoader {
+  static constexpr int NQ = KsOffsets<E, R>::NQ;
+  KsOffsets<E, R> o;
+  const VocabShards* sh;
+  uint64_t stride, col0;
+  const char* base;  // the next step's first row, at the tile's first column
+  uint32_t rows;     // rows of the shard from there on
+  uint32_t c, end;   // padded column of the next step; of the end
+  uint32_t turn;     // where the next shard starts
+  int r;
+  int wave;
+
+  __device__ __forceinline__ void init(const VocabShards& sh_, uint64_t stride_, uint64_t col0_, uint64_t cols,
+                                       uint32_t c_, uint32_t end_, int wave_, int lane) {
+    wave = wave_;
+    sh = &sh_;
     stride = stride_;
     col0 = col0_;
     c = c_;
-    r = 0;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const uint32_t o = (wave + q * NW) * 1024 + lane * 16;
-      const uint32_t k = o / RB;
-      const uint32_t cc = ks_chunk<E>(k, (o % RB) / 16) * 16;
-      krow[q] = k;
-      rel[q] = k * stride + cc;
-      if (cc < cols) in_cols |= 1u << q;
+    end = end_;
+    r = -1;
+    turn = 0;
+    rows = 0;
+    base = nullptr;
+    o.init(static_cast<uint32_t>(stride), cols, wave, lane);
+  }
+  // Before a step: the shard that holds it.
+  __device__ __forceinline__ void prepare() {
+    if (c >= turn && c < end) {
+      do ++r;
+      while (c >= sh->off[r + 1]);  // c < off[p]: ends at the shard that holds c
+      const uint32_t local = c - sh->off[r];
+      turn = sh->off[r + 1];
+      base = uniform(static_cast<const char*>(sh->w[r]) + local * stride + col0);
+      rows = sh->rows[r] > local ? sh->rows[r] - local : 0;
     }
   }
-  __device__ __forceinline__ void step(const VocabShards& sh, char* lds) {
-    while (c >= sh.off[r + 1]) ++r;  // c < off[p]: ends at the shard that holds c
-    const uint32_t local = c - sh.off[r];
-    // rows of the shard from this step on (none in a slot's padded second half)
-    const uint32_t rows = sh.rows[r] > local ? sh.rows[r] - local : 0;
-    const char* b = static_cast<const char*>(sh.w[r]) + local * stride + col0;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const bool in = (in_cols >> q & 1) && krow[q] < rows;
-      load_to_lds(in ? b + rel[q] : reinterpret_cast<const char*>(vocab_zero), lds + base + q * NW * 1024);
-    }
+  __device__ __forceinline__ void load(int q, char* lds) {
+    const uint32_t n = rows < Frag<E>::kBK ? rows : Frag<E>::kBK;
+    const Span m{base, n && c < end ? static_cast<uint32_t>(n * stride - col0) : 0};
+    load_to_lds(m, o.off[q], lds + (wave + q * kWaves) * 1024);
+  }
+  __device__ __forceinline__ void advance() {
     c += Frag<E>::kBK;
+    base += Frag<E>::kBK * stride;
+    rows -= rows < Frag<E>::kBK ? rows : Frag<E>::kBK;
   }
 };
 
@@ -272,45 +348,112 @@ struct KsShardLoader {
 template <int BM_, int BN_, int WM_, int WN_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-  static constexpr int NW = WM * WN;
-  static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
+  static_assert(WM * WN == kWaves, "4 wavefronts");
+  static constexpr int MT = BM / WM / 32, NT = BN / WN / 32;
   static constexpr int ABYTES = BM * 128, BBYTES = BN * 128;
-  static constexpr int STAGE = ABYTES + BBYTES;
+  // LDS: three slots for A's tiles, two for B's (k_loop)
+  static constexpr int LDS = 3 * ABYTES + 2 * BBYTES;
+  static constexpr int BOFF = 3 * ABYTES;
 };
-using T256 = Tile<256, 256, 2, 4>;
+using T256 = Tile<256, 256, 2, 2>;
 using T128 = Tile<128, 128, 2, 2>;
 using T32 = Tile<128, 32, 4, 1>;
 
-// The K loop: two LDS stages, the loads of step k+1 in flight while step k is
-// multiplied.  `issue(lds)` issues the loads of the next step, `fa(tile, m, s)`
-// and `fb(tile, n, s)` read fragments.
-template <class E, class T, class ISSUE, class FA, class FB>
-__device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x4_t (&acc)[T::MT][T::NT], ISSUE issue, FA fa,
+// The K loop.  A step is 128 bytes of k in four quarters.  While a quarter is
+// multiplied the fragments of the next one are read; when those of the last
+// quarter are there, everything in the step's tiles has been read, and the
+// wavefronts meet, once a step.  A has three slots in LDS and B two: A's loads
+// for the step after next go out during the first three quarters, into the free
+// slot, B's during the last one, into the slot just read, so that the loads
+// are spread over the step and have most of a step to arrive.
+// `fa(tile, m, s)` and `fb(tile, n, s)` read the fragments of quarter s.
+//
+// The order within a quarter is the source's: left to itself the compiler reads
+// the fragments where they are used and waits for each.
+// A barrier that leaves memory loads in flight.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+template <int N>
+__device__ __forceinline__ void wait_for_all_but() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <class E, class T, class LA, class LB, class FA, class FB>
+__device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x16_t (&acc)[T::MT][T::NT], LA& la, LB& lb, FA fa,
                                        FB fb) {
+  constexpr int MT = T::MT, NT = T::NT, kMmas = MT * NT;
+  constexpr int kFirst = kMmas > 1 ? kMmas / 2 : 1;        // the products that the reads go between
+  constexpr int kReads = (MT + NT + kFirst - 1) / kFirst;  // fragments read before each of them
 #pragma unroll
-  for (int m = 0; m < T::MT; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < T::NT; ++n) acc[m][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NT; ++n) acc[m][n] = f32x16_t{};
   if (steps == 0) return;
-  issue(lds);
-  __syncthreads();  // waits for the loads as well
-  for (uint32_t k = 0; k < steps; ++k) {
-    char* cur = lds + (k & 1) * T::STAGE;
-    if (k + 1 < steps) issue(lds + ((k + 1) & 1) * T::STAGE);
+  Frag<E> a[2][MT], b[2][NT];
+  const auto read = [&](int to, int i, const char* ta, const char* tb, int s) __attribute__((always_inline)) {
+    if (i < NT) b[to][i] = fb(tb, i, s);
+    else if (i < NT + MT) a[to][i - NT] = fa(ta, i - NT, s);
+  };
+  char* const lds_b = lds + T::BOFF;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      Frag<E> a[T::MT], b[T::NT];
+  for (int i = 0; i < 2; ++i) {
+    la.prepare();
 #pragma unroll
-      for (int n = 0; n < T::NT; ++n) b[n] = fb(cur + T::ABYTES, n, s);
+    for (int q = 0; q < LA::NQ; ++q) la.load(q, lds + i * T::ABYTES);
 #pragma unroll
-      for (int m = 0; m < T::MT; ++m) a[m] = fa(cur, m, s);
-#pragma unroll
-      for (int m = 0; m < T::MT; ++m)
-#pragma unroll
-        for (int n = 0; n < T::NT; ++n) acc[m][n] = mma<E>(a[m], b[n], acc[m][n]);
-    }
-    __syncthreads();
+    for (int q = 0; q < LB::NQ; ++q) lb.load(q, lds_b + i * T::BBYTES);
+    la.advance();
+    lb.advance();
   }
+  wait_for_all_but<LA::NQ + LB::NQ>();
+  meet();
+#pragma unroll
+  for (int i = 0; i < NT + MT; ++i) read(0, i, lds, lds_b, 0);
+  uint32_t slot = 0;  // of A: k mod 3
+  for (uint32_t k = 0; k < steps; ++k) {
+    const uint32_t slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot == 0 ? 2 : slot - 1;
+    const char* const ac = lds + slot * T::ABYTES;
+    const char* const an = lds + slot1 * T::ABYTES;
+    char* const af = lds + slot2 * T::ABYTES;
+    char* const bc = lds_b + (k & 1) * T::BBYTES;
+    const char* const bn = lds_b + (~k & 1) * T::BBYTES;
+    slot = slot1;
+    la.prepare();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      if (s == 3) {
+        wait_for_all_but<LA::NQ>();
+        meet();
+      }
+#pragma unroll
+      for (int i = 0; i < kMmas; ++i) {
+#pragma unroll
+        for (int j = i * kReads; j < (i + 1) * kReads; ++j) {
+          if (s < 3) read(~s & 1, j, ac, bc, s + 1);
+          else read(0, j, an, bn, 0);  // after the last step: what lies there, unused
+        }
+        // loads past the last step read zeros, unused
+        if (s < 3) {
+          constexpr int kAll = 3 * kMmas;
+          const int at = s * kMmas + i;
+#pragma unroll
+          for (int q = at * LA::NQ / kAll; q < (at + 1) * LA::NQ / kAll; ++q) la.load(q, af);
+        } else {
+#pragma unroll
+          for (int q = i * LB::NQ / kMmas; q < (i + 1) * LB::NQ / kMmas; ++q) lb.load(q, bc);
+        }
+        acc[i / NT][i % NT] = mma<E>(a[s & 1][i / NT], b[s & 1][i % NT], acc[i / NT][i % NT]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    la.advance();
+    lb.advance();
+  }
+  wait_for_loads();
+  __syncthreads();  // the caller may use the LDS
 }
 
 // Workgroup -> tile.  Consecutive workgroups go to the 8 XCDs in turn, so each
@@ -329,11 +472,46 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tm, uint32_t tn, u
 }
 
 // ---------------------------------------------------------------------------
+// 16-bit results on their way out.  A lane of the accumulators holds 4
+// consecutive values of M for one N, 8 bytes: written as they are, every
+// instruction would touch 32 rows of the output for 16 bytes each.  They are laid
+// down in LDS as rows of M instead (16 bytes of padding keep neighbouring rows
+// in different banks), and leave as 16 bytes a lane along the rows.
+template <class T>
+constexpr uint32_t kRow16 = T::BM * 2 + 16;
+
+template <class E, class T>
+__device__ __forceinline__ void put16(char* lds, uint32_t n, uint32_t m, const float* v, uint32_t mask) {
+  static_assert(T::BN * kRow16<T> <= T::LDS, "the tile fits");
+  uint32_t w0, w1;
+  if constexpr (__is_same(E, EBF16)) {
+    w0 = f32x2_to_bf16x2_bits(v[0], v[1]);
+    w1 = f32x2_to_bf16x2_bits(v[2], v[3]);
+  } else {
+    w0 = f32x2_to_f16x2_bits(v[0], v[1]);
+    w1 = f32x2_to_f16x2_bits(v[2], v[3]);
+  }
+  *reinterpret_cast<uint2*>(lds + n * kRow16<T> + m * 2) = make_uint2(w0 & mask, w1 & mask);
+}
+
+// out(n, m): where the 8 values from m on of row n go, or NULL.
+template <class E, class T, class OUT>
+__device__ __forceinline__ void take16(const char* lds, OUT out) {
+  constexpr uint32_t kChunks = T::BM / 8, kRows = kWaves * 64 / kChunks;
+  const uint32_t c = threadIdx.x % kChunks;
+#pragma unroll 4
+  for (uint32_t n = threadIdx.x / kChunks; n < T::BN; n += kRows) {
+    char* q = out(n, c * 8);
+    if (q) *reinterpret_cast<u32x4*>(q) = *reinterpret_cast<const u32x4*>(lds + n * kRow16<T> + c * 16);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Logits: M = vocabulary, N = tokens.  A lane of an accumulator holds 4
 // consecutive columns of one token.
 template <class E, class T, bool GRAD>
-__global__ __launch_bounds__(T::NW * 64) void k_logits(LogitArgs a) {
-  __shared__ __attribute__((aligned(128))) char lds[2 * T::STAGE];
+__global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
+  __shared__ __attribute__((aligned(128))) char lds[T::LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint32_t tm, tn;
@@ -341,64 +519,66 @@ __global__ __launch_bounds__(T::NW * 64) void k_logits(LogitArgs a) {
   const uint32_t cbase = a.c0 + tm * T::BM;
   const uint32_t t0 = tn * T::BN;
 
-  KcLoader<T::BM, T::NW> la;
-  KcLoader<T::BN, T::NW> lb;
-  la.init(
-      [&](uint32_t row) -> const char* {
-        const uint32_t c = cbase + row;
-        const char* q = nullptr;
-        for (int r = 0; r < a.sh.p; ++r)
-          if (c >= a.sh.off[r] && c - a.sh.off[r] < a.sh.rows[r])
-            q = static_cast<const char*>(a.sh.w[r]) + static_cast<uint64_t>(c - a.sh.off[r]) * a.w_stride;
-        return c < a.c1 ? q : nullptr;
-      },
-      a.kbytes, wave, lane);
-  lb.init(
-      [&](uint32_t row) -> const char* {
-        const uint32_t t = t0 + row;
-        return t < a.tokens ? static_cast<const char*>(a.x) + t * a.x_stride : nullptr;
-      },
-      a.kbytes, wave, lane);
-  f32x4_t acc[T::MT][T::NT];
+  KcShardLoader<T::BM> la;
+  KcLoader<T::BN> lb;
+  la.init(a.sh, a.w_stride, cbase, a.c1, a.kbytes, wave, lane);
+  lb.init(a.x, a.x_stride, t0, a.tokens, a.kbytes, 0, wave, lane);
+  f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
-  const int m0 = wm * (T::MT * 16), n0 = wn * (T::NT * 16);
+  const int m0 = wm * (T::MT * 32), n0 = wn * (T::NT * 32);
   k_loop<E, T>(
-      lds, (a.kbytes + 127) / 128, acc,
-      [&](char* l) {
-        la.step(l);
-        lb.step(l + T::ABYTES);
-      },
-      [&](const char* t, int m, int s) { return frag_kc<E>(t, m0 + m * 16, s, lane); },
-      [&](const char* t, int n, int s) { return frag_kc<E>(t, n0 + n * 16, s, lane); });
+      lds, (a.kbytes + 127) / 128, acc, la, lb,
+      [&](const char* t, int m, int s) { return frag_kc<E>(t, m0 + m * 32, s, lane); },
+      [&](const char* t, int n, int s) { return frag_kc<E>(t, n0 + n * 32, s, lane); });
 
-  // Which of this lane's 4 columns per M fragment exist: bit 4m + j.
-  const uint32_t lc = cbase + m0 + (lane >> 4) * 4;
-  uint32_t have = 0;
-  for (int r = 0; r < a.sh.p; ++r) {
-    const uint32_t lo = a.sh.off[r], hi = lo + a.sh.rows[r];
+  // Column of register 4i + j of fragment m: lc + 32 m + 8 i + j.  Columns that pad
+  // a slot have no logit; most tiles have none of them.
+  const uint32_t cw = cbase + m0, half = (lane >> 5) * 4, lc = cw + half;
+  uint32_t lim[T::MT];  // lc + 32 m + x exists for x < lim[m]
+  bool full = true;
+#pragma unroll
+  for (int m = 0; m < T::MT; ++m) {
+    const uint32_t c = cw + m * 32;
+    uint32_t end = 0;
+    for (int r = 0; r < a.sh.p; ++r)
+      if (c >= a.sh.off[r] && c < a.sh.off[r + 1]) end = a.sh.off[r] + a.sh.rows[r];
+    end = end < a.c1 ? end : a.c1;
+    lim[m] = end > c + half ? end - (c + half) : 0;
+    full = full && end >= c + 32;
+  }
+  if (!full) {
 #pragma unroll
     for (int m = 0; m < T::MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t c = lc + m * 16 + j;
-        if (c >= lo && c < hi && c < a.c1) have |= 1u << (4 * m + j);
-      }
+      for (int n = 0; n < T::NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (static_cast<uint32_t>(x / 4 * 8 + x % 4) >= lim[m]) acc[m][n][x] = -__builtin_inff();
   }
+  // The logit `rel` columns from lc in fragment column n, if this lane holds it.
+  const auto pick = [&](int n, uint32_t rel, float& z) __attribute__((always_inline)) {
+    bool here = false;
+#pragma unroll
+    for (int m = 0; m < T::MT; ++m)
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        if (rel == static_cast<uint32_t>(m * 32 + x / 4 * 8 + x % 4)) {
+          z = acc[m][n][x];
+          here = true;
+        }
+    return here;
+  };
 
   if constexpr (!GRAD) {
     float* red = reinterpret_cast<float*>(lds);  // [WM][BN][2]
 #pragma unroll
     for (int n = 0; n < T::NT; ++n) {
-      const uint32_t t = t0 + n0 + n * 16 + (lane & 15);
+      const uint32_t t = t0 + n0 + n * 32 + (lane & 31);
       float mx = -__builtin_inff();
 #pragma unroll
       for (int m = 0; m < T::MT; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (!(have >> (4 * m + j) & 1)) acc[m][n][j] = -__builtin_inff();
-          mx = fmaxf(mx, acc[m][n][j]);
-        }
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
+        for (int x = 0; x < 16; ++x) mx = fmaxf(mx, acc[m][n][x]);
       mx = fmaxf(mx, __shfl_xor(mx, 32));
       // a tile whose logits are all -inf has sum 0, not NaN
       const float ref = mx == -__builtin_inff() ? 0.f : mx;
@@ -406,25 +586,21 @@ __global__ __launch_bounds__(T::NW * 64) void k_logits(LogitArgs a) {
 #pragma unroll
       for (int m = 0; m < T::MT; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum += __expf(acc[m][n][j] - ref);
-      sum += __shfl_xor(sum, 16);
+        for (int x = 0; x < 16; ++x) sum += __expf(acc[m][n][x] - ref);
       sum += __shfl_xor(sum, 32);
-      if (lane < 16) {
-        float* q = red + (wm * T::BN + n0 + n * 16 + lane) * 2;
+      if (lane < 32) {
+        float* q = red + (wm * T::BN + n0 + n * 32 + lane) * 2;
         q[0] = mx;
         q[1] = sum;
       }
       if (t < a.tokens) {
         const uint32_t col = padded_col(a.sh, target_at(a.targets, a.target_bytes, t));
-#pragma unroll
-        for (int m = 0; m < T::MT; ++m)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (col == lc + m * 16 + j && (have >> (4 * m + j) & 1)) a.hit[t] = acc[m][n][j];
+        float z;
+        if (col - cw < T::MT * 32 && pick(n, col - lc, z)) a.hit[t] = z;  // few tiles hold a token's target
       }
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < T::BN; i += T::NW * 64) {
+    for (uint32_t i = threadIdx.x; i < T::BN; i += kWaves * 64) {
       const uint32_t t = t0 + i;
       if (t >= a.tokens) continue;
       float mx = red[i * 2], sum = red[i * 2 + 1];
@@ -444,8 +620,7 @@ __global__ __launch_bounds__(T::NW * 64) void k_logits(LogitArgs a) {
     using S = typename E::S;
 #pragma unroll
     for (int n = 0; n < T::NT; ++n) {
-      const uint32_t t = t0 + n0 + n * 16 + (lane & 15);
-      if (t >= a.grad_rows) continue;
+      const uint32_t tl = n0 + n * 32 + (lane & 31), t = t0 + tl;
       uint32_t col = kMasked;
       float lse = 0.f, g = 0.f;
       if (t < a.tokens) {
@@ -453,55 +628,61 @@ __global__ __launch_bounds__(T::NW * 64) void k_logits(LogitArgs a) {
         lse = a.lse[t];
         g = a.grad_loss[t];
       }
-      const bool live = col != kMasked;
+      const uint32_t live = col != kMasked ? ~0u : 0u;
       if constexpr (__is_same(E, EF16)) g = ldexpf(g, 15 - token_exponent(g));
-      S* out = static_cast<S*>(a.grad) + t * a.ld;
+      float zt = 0.f;
+      const bool hot = live && col - cw < T::MT * 32 && pick(n, col - lc, zt);
 #pragma unroll
-      for (int m = 0; m < T::MT; ++m) {
-        float v[4];
+      for (int m = 0; m < T::MT; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float pr = __expf(acc[m][n][j] - lse) - (col == lc + m * 16 + j ? 1.f : 0.f);
-          v[j] = live && (have >> (4 * m + j) & 1) ? pr * g : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          float v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = __expf(acc[m][n][4 * i + j] - lse) * g;
+          if constexpr (sizeof(S) == 2) {
+            put16<E, T>(lds, tl, m0 + m * 32 + i * 8 + half, v, live);
+          } else {
+            const uint32_t c = lc + m * 32 + i * 8;
+            if (t < a.grad_rows && c < a.c1) {
+              u32x4 w;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(v[j]) & live;
+              *reinterpret_cast<u32x4*>(static_cast<S*>(a.grad) + t * a.ld + (c - a.c0)) = w;
+            }
+          }
         }
-        const uint32_t c = lc + m * 16 - a.c0;
+      if (hot) {
+        const float x = (__expf(zt - lse) - 1.f) * g;
         if constexpr (sizeof(S) == 2) {
           // The target's entry is the row's largest by far; what its rounding
-          // takes goes into the two products on the side (k_join,
+          // takes goes into the two products on the side (HiddenRow,
           // k_weight_grad), which leaves the rounding of the outputs the
           // largest error.
-          const uint32_t j = col - (lc + m * 16);
-          if (live && j < 4) {
-            const float x = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
-            a.lo[t] = x - half_to_f32<E>(f32_to_half<E>(x));
-          }
-        }
-        if (c < a.c1 - a.c0) {
-          if constexpr (sizeof(S) == 4) {
-            *reinterpret_cast<f32x4_t*>(out + c) = f32x4_t{v[0], v[1], v[2], v[3]};
-          } else {
-            uint32_t w0, w1;
-            if constexpr (__is_same(E, EBF16)) {
-              w0 = f32x2_to_bf16x2_bits(v[0], v[1]);
-              w1 = f32x2_to_bf16x2_bits(v[2], v[3]);
-            } else {
-              w0 = f32x2_to_f16x2_bits(v[0], v[1]);
-              w1 = f32x2_to_f16x2_bits(v[2], v[3]);
-            }
-            *reinterpret_cast<uint2*>(out + c) = make_uint2(w0, w1);
-          }
+          const uint32_t b = f32_to_half<E>(x);
+          *reinterpret_cast<S*>(lds + tl * kRow16<T> + (col - cbase) * 2) = static_cast<S>(b);
+          a.lo[t] = x - half_to_f32<E>(b);
+        } else {
+          static_cast<S*>(a.grad)[t * a.ld + (col - a.c0)] = x;
         }
       }
+    }
+    if constexpr (sizeof(S) == 2) {
+      __syncthreads();
+      take16<E, T>(lds, [&](uint32_t row, uint32_t m) -> char* {
+        const uint32_t t = t0 + row, c = cbase + m;
+        return t < a.grad_rows && c < a.c1 ? reinterpret_cast<char*>(static_cast<S*>(a.grad) + t * a.ld + (c - a.c0))
+                                           : nullptr;
+      });
     }
   }
 }
 
 // ---------------------------------------------------------------------------
 // dhidden: M = dim, N = tokens, K = the piece's padded columns, in `splits`
-// parts.  Accumulated in float32.
+// parts.  Where that is all of K the result is written, else float32 sums.
 template <class E, class T>
-__global__ __launch_bounds__(T::NW * 64) void k_hidden_grad(HiddenGradArgs a) {
-  __shared__ __attribute__((aligned(128))) char lds[2 * T::STAGE];
+__global__ __launch_bounds__(kWaves * 64) void k_hidden_grad(HiddenGradArgs a) {
+  __shared__ __attribute__((aligned(128))) char lds[T::LDS];
   constexpr int esz = sizeof(typename E::S);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -514,49 +695,89 @@ __global__ __launch_bounds__(T::NW * 64) void k_hidden_grad(HiddenGradArgs a) {
   const uint32_t k_lo = static_cast<uint64_t>(all) * split / a.splits;
   const uint32_t k_hi = static_cast<uint64_t>(all) * (split + 1) / a.splits;
 
-  KsShardLoader<E, T::BM, T::NW> la;
-  KcLoader<T::BN, T::NW> lb;
+  KsShardLoader<E, T::BM> la;
+  KcLoader<T::BN> lb;
   la.init(a.sh, a.w_stride, static_cast<uint64_t>(d0) * esz, static_cast<uint64_t>(a.dim - d0) * esz,
-          a.c0 + k_lo * Frag<E>::kBK, wave, lane);
-  lb.init(
-      [&](uint32_t row) -> const char* {
-        const uint32_t t = t0 + row;
-        return t < a.grad_rows ? static_cast<const char*>(a.grad) + t * a.ld * esz : nullptr;
-      },
-      (a.c1 - a.c0) * esz, wave, lane);
-  lb.seek(k_lo);
-  f32x4_t acc[T::MT][T::NT];
+          a.c0 + k_lo * Frag<E>::kBK, a.c0 + k_hi * Frag<E>::kBK, wave, lane);
+  lb.init(a.grad, a.ld * esz, t0, a.grad_rows, (a.c1 - a.c0) * esz, k_lo, wave, lane);
+  f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
-  const int m0 = wm * (T::MT * 16), n0 = wn * (T::NT * 16);
+  const int m0 = wm * (T::MT * 32), n0 = wn * (T::NT * 32);
   k_loop<E, T>(
-      lds, k_hi - k_lo, acc,
-      [&](char* l) {
-        la.step(a.sh, l);
-        lb.step(l + T::ABYTES);
-      },
-      [&](const char* t, int m, int s) { return frag_ks<E, T::BM>(t, m0 + m * 16, s, lane); },
-      [&](const char* t, int n, int s) { return frag_kc<E>(t, n0 + n * 16, s, lane); });
+      lds, k_hi - k_lo, acc, la, lb,
+      [&](const char* t, int m, int s) { return frag_ks<E, T::BM>(t, m0 + m * 32, s, lane); },
+      [&](const char* t, int n, int s) { return frag_kc<E>(t, n0 + n * 32, s, lane); });
+  using S = typename E::S;
+  if (a.out) {
+    // the whole vocabulary in one product: the result itself
+#pragma unroll
+    for (int n = 0; n < T::NT; ++n) {
+      const uint32_t tl = n0 + n * 32 + (lane & 31), t = t0 + tl;
+      const HiddenRow<E> h(a.sh, a.tcol, a.lo, a.grad_loss, t, a.tokens, a.dim);
+#pragma unroll
+      for (int m = 0; m < T::MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t dl = m0 + m * 32 + i * 8 + (lane >> 5) * 4, d = d0 + dl;
+          float v[4] = {acc[m][n][4 * i], acc[m][n][4 * i + 1], acc[m][n][4 * i + 2], acc[m][n][4 * i + 3]};
+          if constexpr (esz == 2) {
+            h.finish4(v, d, a.dim);
+            put16<E, T>(lds, tl, dl, v, h.live ? ~0u : 0u);
+          } else if (t < a.tokens && d < a.dim) {
+            u32x4 w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = h.live ? __float_as_uint(v[j]) : 0u;
+            *reinterpret_cast<u32x4*>(static_cast<S*>(a.out) + static_cast<uint64_t>(t) * a.dim + d) = w;
+          }
+        }
+    }
+    if constexpr (esz == 2) {
+      __syncthreads();
+      take16<E, T>(lds, [&](uint32_t n, uint32_t m) -> char* {
+        const uint32_t t = t0 + n, d = d0 + m;
+        return t < a.tokens && d < a.dim
+                   ? reinterpret_cast<char*>(static_cast<S*>(a.out) + static_cast<uint64_t>(t) * a.dim + d)
+                   : nullptr;
+      });
+    }
+    return;
+  }
   float* out = a.acc + split * a.split_stride;
+  const bool vec = a.dim % 4 == 0;
 #pragma unroll
   for (int n = 0; n < T::NT; ++n) {
-    const uint32_t t = t0 + n0 + n * 16 + (lane & 15);
+    const uint32_t t = t0 + n0 + n * 32 + (lane & 31);
     if (t >= a.tokens) continue;
 #pragma unroll
-    for (int m = 0; m < T::MT; ++m) {
-      const uint32_t d = d0 + m0 + m * 16 + (lane >> 4) * 4;
-      float* q = out + static_cast<uint64_t>(t) * a.dim + d;
+    for (int m = 0; m < T::MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (d + j < a.dim) q[j] = a.add ? q[j] + acc[m][n][j] : acc[m][n][j];
-    }
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t d = d0 + m0 + m * 32 + i * 8 + (lane >> 5) * 4;
+        float* q = out + static_cast<uint64_t>(t) * a.dim + d;
+        if (vec) {
+          if (d < a.dim) {
+            f32x4_t v = {acc[m][n][4 * i], acc[m][n][4 * i + 1], acc[m][n][4 * i + 2], acc[m][n][4 * i + 3]};
+            if (a.add) {
+              const f32x4_t o = *reinterpret_cast<const f32x4_t*>(q);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[j] += o[j];
+            }
+            *reinterpret_cast<f32x4_t*>(q) = v;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (d + j < a.dim) q[j] = a.add ? q[j] + acc[m][n][4 * i + j] : acc[m][n][4 * i + j];
+        }
+      }
   }
 }
 
 // ---------------------------------------------------------------------------
 // dweights: M = dim, N = the piece's padded columns, K = tokens.
 template <class E, class T>
-__global__ __launch_bounds__(T::NW * 64) void k_weight_grad(WeightGradArgs a) {
-  __shared__ __attribute__((aligned(128))) char lds[2 * T::STAGE];
+__global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
+  __shared__ __attribute__((aligned(128))) char lds[T::LDS];
   using S = typename E::S;
   constexpr int esz = sizeof(S);
   const int lane = threadIdx.x & 63;
@@ -564,58 +785,54 @@ __global__ __launch_bounds__(T::NW * 64) void k_weight_grad(WeightGradArgs a) {
   uint32_t tm, tn;
   tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
   const uint32_t d0 = tm * T::BM, v0 = tn * T::BN;
-  KsLoader<E, T::BM, T::NW> la;
-  KsLoader<E, T::BN, T::NW> lb;
-  la.init(static_cast<const char*>(a.xg) + static_cast<uint64_t>(d0) * esz, a.xg_stride,
-          a.xg_stride - static_cast<uint64_t>(d0) * esz, 0, wave, lane);
+  KsLoader<E, T::BM> la;
+  KsLoader<E, T::BN> lb;
+  const char* const xg = static_cast<const char*>(a.xg) + static_cast<uint64_t>(d0) * esz;
+  const uint64_t xg_cols = a.xg_stride - static_cast<uint64_t>(d0) * esz;
+  la.init(xg, a.xg_stride, xg_cols, a.rows / Frag<E>::kBK, wave, lane);
   lb.init(static_cast<const char*>(a.grad) + static_cast<uint64_t>(v0) * esz, a.ld * esz,
-          static_cast<uint64_t>(a.c1 - a.c0 - v0) * esz, 0, wave, lane);
-  f32x4_t acc[T::MT][T::NT];
+          static_cast<uint64_t>(a.c1 - a.c0 - v0) * esz, a.rows / Frag<E>::kBK, wave, lane);
+  f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
-  const int m0 = wm * (T::MT * 16), n0 = wn * (T::NT * 16);
+  const int m0 = wm * (T::MT * 32), n0 = wn * (T::NT * 32);
   k_loop<E, T>(
-      lds, a.rows / Frag<E>::kBK, acc,
-      [&](char* l) {
-        la.step(l);
-        lb.step(l + T::ABYTES);
-      },
-      [&](const char* t, int m, int s) { return frag_ks<E, T::BM>(t, m0 + m * 16, s, lane); },
-      [&](const char* t, int n, int s) { return frag_ks<E, T::BN>(t, n0 + n * 16, s, lane); });
+      lds, a.rows / Frag<E>::kBK, acc, la, lb,
+      [&](const char* t, int m, int s) { return frag_ks<E, T::BM>(t, m0 + m * 32, s, lane); },
+      [&](const char* t, int n, int s) { return frag_ks<E, T::BN>(t, n0 + n * 32, s, lane); });
   if constexpr (esz == 2) {
     // What rounding took from the targets' entries: the tokens whose target
     // lies in this tile (few: the whole vocabulary shares the tokens) are
     // listed in order and added as further K steps of 64.
-    __shared__ uint32_t list[64 + T::NW * 64];
-    __shared__ uint32_t found[T::NW];
+    uint32_t* const list = reinterpret_cast<uint32_t*>(lds + T::ABYTES);  // 64 + kWaves * 64
+    uint32_t* const found = list + 64 + kWaves * 64;
     const uint32_t first = a.c0 + v0;
     uint32_t have = 0;
     const auto add = [&](uint32_t n) {
-#pragma unroll
-      for (int q = 0; q < KsLoader<E, T::BM, T::NW>::NQ; ++q) {
-        const uint32_t o = (wave + q * T::NW) * 1024 + lane * 16;
-        const uint32_t k = o / (T::BM * esz);
-        const uint32_t c = ks_chunk<E>(k, (o % (T::BM * esz)) / 16) * 16;
-        const bool in = k < n && c < a.xg_stride - static_cast<uint64_t>(d0) * esz;
-        load_to_lds(in ? static_cast<const char*>(a.xg) + list[k] * a.xg_stride + static_cast<uint64_t>(d0) * esz + c
-                       : reinterpret_cast<const char*>(vocab_zero),
-                    lds + o - lane * 16);
+      // rows of different tokens: the list's row k, this lane's chunk
+      constexpr uint32_t RB = T::BM * esz;
+      for (uint32_t i = threadIdx.x; i < T::ABYTES / 16; i += kWaves * 64) {
+        const uint32_t k = i * 16 / RB;
+        const uint32_t c = ks_chunk<E>(k, (i * 16 % RB) / 16) * 16;
+        u32x4 v{0, 0, 0, 0};
+        if (k < n && c < xg_cols) v = *reinterpret_cast<const u32x4*>(xg + list[k] * a.xg_stride + c);
+        *reinterpret_cast<u32x4*>(lds + i * 16) = v;
       }
-      for (uint32_t i = threadIdx.x; i < T::BBYTES / 16; i += T::NW * 64)
-        *reinterpret_cast<u32x4*>(lds + T::ABYTES + i * 16) = u32x4{0, 0, 0, 0};
+      for (uint32_t i = threadIdx.x; i < T::BBYTES / 16; i += kWaves * 64)
+        *reinterpret_cast<u32x4*>(lds + T::BOFF + i * 16) = u32x4{0, 0, 0, 0};
       __syncthreads();
       if (threadIdx.x < n) {
         const uint32_t k = threadIdx.x, t = list[k], c = a.tcol[t] - first;
         const uint32_t at = k * (T::BN * esz) + (((c >> 4) ^ ks_swizzle<E>(k)) << 5) + (c & 15u) * 2;
-        *reinterpret_cast<S*>(lds + T::ABYTES + at) = static_cast<S>(f32_to_half<E>(a.lo[t]));
+        *reinterpret_cast<S*>(lds + T::BOFF + at) = static_cast<S>(f32_to_half<E>(a.lo[t]));
       }
       __syncthreads();
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 4; ++s) {
         Frag<E> fa[T::MT], fb[T::NT];
 #pragma unroll
-        for (int m = 0; m < T::MT; ++m) fa[m] = frag_ks<E, T::BM>(lds, m0 + m * 16, s, lane);
+        for (int m = 0; m < T::MT; ++m) fa[m] = frag_ks<E, T::BM>(lds, m0 + m * 32, s, lane);
 #pragma unroll
-        for (int n2 = 0; n2 < T::NT; ++n2) fb[n2] = frag_ks<E, T::BN>(lds + T::ABYTES, n0 + n2 * 16, s, lane);
+        for (int n2 = 0; n2 < T::NT; ++n2) fb[n2] = frag_ks<E, T::BN>(lds + T::BOFF, n0 + n2 * 32, s, lane);
 #pragma unroll
         for (int m = 0; m < T::MT; ++m)
 #pragma unroll
@@ -623,7 +840,7 @@ __global__ __launch_bounds__(T::NW * 64) void k_weight_grad(WeightGradArgs a) {
       }
       __syncthreads();
     };
-    for (uint32_t b = 0; b < a.tokens; b += T::NW * 64) {
+    for (uint32_t b = 0; b < a.tokens; b += kWaves * 64) {
       const uint32_t t = b + threadIdx.x;
       const bool in = t < a.tokens && a.tcol[t] - first < T::BN;  // kMasked - first is out of range
       const uint64_t mask = __ballot(in);
@@ -631,7 +848,7 @@ __global__ __launch_bounds__(T::NW * 64) void k_weight_grad(WeightGradArgs a) {
       __syncthreads();
       uint32_t at = have, total = have;
 #pragma unroll
-      for (int w = 0; w < T::NW; ++w) {
+      for (int w = 0; w < kWaves; ++w) {
         if (w < wave) at += found[w];
         total += found[w];
       }
@@ -652,25 +869,55 @@ __global__ __launch_bounds__(T::NW * 64) void k_weight_grad(WeightGradArgs a) {
   }
   float scale = 1.f;
   if constexpr (__is_same(E, EF16)) scale = ldexpf(1.f, a.scale[0] - 15);
-#pragma unroll
-  for (int n = 0; n < T::NT; ++n) {
-    const uint32_t c = a.c0 + v0 + n0 + n * 16 + (lane & 15);
+  // row n of the tile: a vocabulary row of one of the shards
+  const auto row_of = [&](uint32_t n) -> S* {
+    const uint32_t c = a.c0 + v0 + n;
     S* row = nullptr;
     if (c < a.c1)
       for (int r = 0; r < a.sh.p; ++r)
         if (c >= a.sh.off[r] && c - a.sh.off[r] < a.sh.rows[r])
           row = static_cast<S*>(a.dw[r]) + static_cast<uint64_t>(c - a.sh.off[r]) * a.dim;
+    return row;
+  };
+  if (esz == 2 && a.vec) {
+#pragma unroll
+    for (int n = 0; n < T::NT; ++n)
+#pragma unroll
+      for (int m = 0; m < T::MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = acc[m][n][4 * i + j] * scale;
+          if constexpr (esz == 2)
+            put16<E, T>(lds, n0 + n * 32 + (lane & 31), m0 + m * 32 + i * 8 + (lane >> 5) * 4, v, ~0u);
+        }
+    __syncthreads();
+    take16<E, T>(lds, [&](uint32_t n, uint32_t m) -> char* {
+      S* row = d0 + m < a.dim ? row_of(n) : nullptr;
+      return row ? reinterpret_cast<char*>(row + d0 + m) : nullptr;
+    });
+    return;
+  }
+#pragma unroll
+  for (int n = 0; n < T::NT; ++n) {
+    S* row = row_of(n0 + n * 32 + (lane & 31));
     if (!row) continue;
 #pragma unroll
-    for (int m = 0; m < T::MT; ++m) {
-      const uint32_t d = d0 + m0 + m * 16 + (lane >> 4) * 4;
-      float v[4];
+    for (int m = 0; m < T::MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = acc[m][n][j] * scale;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t d = d0 + m0 + m * 32 + i * 8 + (lane >> 5) * 4;
+        if (esz == 4 && a.vec) {
+          if (d < a.dim)
+            *reinterpret_cast<f32x4_t*>(row + d) =
+                f32x4_t{acc[m][n][4 * i], acc[m][n][4 * i + 1], acc[m][n][4 * i + 2], acc[m][n][4 * i + 3]};
+        } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (d + j < a.dim) store_one<E>(row + d + j, v[j]);
-    }
+          for (int j = 0; j < 4; ++j)
+            if (d + j < a.dim) store_one<E>(row + d + j, acc[m][n][4 * i + j] * scale);
+        }
+      }
   }
 }
 
@@ -681,9 +928,9 @@ hipError_t run_logits(const LogitArgs& a, VocabTile t, bool grad, hipStream_t s)
   if (g.x == 0) return hipSuccess;
 #define RR_LAUNCH(TT)                                                        \
   if (grad)                                                                  \
-    hipLaunchKernelGGL((k_logits<E, TT, true>), g, dim3(TT::NW * 64), 0, s, a); \
+    hipLaunchKernelGGL((k_logits<E, TT, true>), g, dim3(kWaves * 64), 0, s, a); \
   else                                                                       \
-    hipLaunchKernelGGL((k_logits<E, TT, false>), g, dim3(TT::NW * 64), 0, s, a);
+    hipLaunchKernelGGL((k_logits<E, TT, false>), g, dim3(kWaves * 64), 0, s, a);
   switch (t) {
     case VocabTile::k256x256: RR_LAUNCH(T256) break;
     case VocabTile::k128x128: RR_LAUNCH(T128) break;
@@ -698,9 +945,9 @@ hipError_t run_hidden_grad(const HiddenGradArgs& a, VocabTile t, hipStream_t s) 
   const dim3 g(a.tiles_m * a.tiles_n * a.splits);
   if (g.x == 0) return hipSuccess;
   switch (t) {
-    case VocabTile::k256x256: hipLaunchKernelGGL((k_hidden_grad<E, T256>), g, dim3(T256::NW * 64), 0, s, a); break;
-    case VocabTile::k128x128: hipLaunchKernelGGL((k_hidden_grad<E, T128>), g, dim3(T128::NW * 64), 0, s, a); break;
-    default: hipLaunchKernelGGL((k_hidden_grad<E, T32>), g, dim3(T32::NW * 64), 0, s, a); break;
+    case VocabTile::k256x256: hipLaunchKernelGGL((k_hidden_grad<E, T256>), g, dim3(kWaves * 64), 0, s, a); break;
+    case VocabTile::k128x128: hipLaunchKernelGGL((k_hidden_grad<E, T128>), g, dim3(kWaves * 64), 0, s, a); break;
+    default: hipLaunchKernelGGL((k_hidden_grad<E, T32>), g, dim3(kWaves * 64), 0, s, a); break;
   }
   return hipGetLastError();
 }
@@ -710,9 +957,9 @@ hipError_t run_weight_grad(const WeightGradArgs& a, VocabTile t, hipStream_t s) 
   const dim3 g(a.tiles_m * a.tiles_n);
   if (g.x == 0) return hipSuccess;
   if (t == VocabTile::k256x256)
-    hipLaunchKernelGGL((k_weight_grad<E, T256>), g, dim3(T256::NW * 64), 0, s, a);
+    hipLaunchKernelGGL((k_weight_grad<E, T256>), g, dim3(kWaves * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((k_weight_grad<E, T128>), g, dim3(T128::NW * 64), 0, s, a);
+    hipLaunchKernelGGL((k_weight_grad<E, T128>), g, dim3(kWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 
