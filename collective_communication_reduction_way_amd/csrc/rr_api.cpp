@@ -1396,6 +1396,13 @@ size_t rr_vocab_cross_entropy_workspace_size(int p, size_t tokens, size_t dim, s
   return std::max(aligned.total, packed.total);
 }
 
+// The widest of 16, 8, 4 and 2 bytes that rows of row_bytes from these addresses are aligned to.
+static uint32_t align_unit(const std::vector<uintptr_t>& addrs, uint64_t row_bytes) {
+  uintptr_t acc = static_cast<uintptr_t>(row_bytes);
+  for (uintptr_t a : addrs) acc |= a;
+  return acc % 16 == 0 ? 16 : acc % 8 == 0 ? 8 : acc % 4 == 0 ? 4 : 2;
+}
+
 // The piece's columns and, when the inputs are copied first, its weight rows:
 // sh.w[r] then points where row 0 of shard r would lie (only rows of the piece
 // are read).
@@ -1408,6 +1415,10 @@ static hipError_t vocab_piece(const rr::VocabPlan& pl, const rr::VocabShards& sh
   a.sh = sh;
   a.out = ws + pl.pack_w;
   a.out_stride = row;
+  std::vector<uintptr_t> addrs;
+  for (int r = 0; r < sh.p; ++r)
+    if (sh.rows[r]) addrs.push_back(reinterpret_cast<uintptr_t>(sh.w[r]));
+  a.unit = align_unit(addrs, static_cast<uint64_t>(pl.dim) * pl.esz);
   a.dim = pl.dim;
   a.c0 = c0;
   a.c1 = c1;
@@ -1420,6 +1431,45 @@ static hipError_t vocab_piece(const rr::VocabPlan& pl, const rr::VocabShards& sh
 }
 
 static uint32_t tiles_over(uint64_t n, uint32_t t) { return static_cast<uint32_t>((n + t - 1) / t); }
+
+// The logits of the columns [c0, c1) for `rows` tokens: large tiles and, for a last
+// round that would leave most of the chip idle, small ones.
+static hipError_t vocab_logits(rr::LogitArgs& a, Kind k, rr::VocabTile t, bool grad, uint32_t c0, uint32_t c1,
+                               uint32_t rows, hipStream_t s) {
+  const uint32_t cm = rr::tail_start(c0, c1, tiles_over(rows, 256), t);
+  char* const g = static_cast<char*>(a.grad);
+  for (int tail = 0; tail < 2; ++tail) {
+    const rr::VocabTile tt = tail ? rr::VocabTile::k128x128 : t;
+    a.c0 = tail ? cm : c0;
+    a.c1 = tail ? c1 : cm;
+    if (a.c0 == a.c1) continue;
+    a.grad = grad ? g + static_cast<uint64_t>(a.c0 - c0) * (k == Kind::kF32 ? 4 : 2) : nullptr;
+    a.tiles_m = tiles_over(a.c1 - a.c0, rr::tile_m(tt));
+    a.tiles_n = tiles_over(rows, rr::tile_n(tt));
+    const hipError_t e = rr::launch_logits(a, k, tt, grad, s);
+    if (e != hipSuccess) return e;
+    a.tile0 += a.tiles_m;
+  }
+  return hipSuccess;
+}
+
+static hipError_t vocab_weight_grad(rr::WeightGradArgs& w, Kind k, rr::VocabTile t, uint32_t c0, uint32_t c1,
+                                    hipStream_t s) {
+  const uint32_t cm = rr::tail_start(c0, c1, tiles_over(w.dim, 256), t);
+  const char* const g = static_cast<const char*>(w.grad);
+  for (int tail = 0; tail < 2; ++tail) {
+    const rr::VocabTile tt = tail ? rr::VocabTile::k128x128 : t;
+    w.c0 = tail ? cm : c0;
+    w.c1 = tail ? c1 : cm;
+    if (w.c0 == w.c1) continue;
+    w.grad = g + static_cast<uint64_t>(w.c0 - c0) * (k == Kind::kF32 ? 4 : 2);
+    w.tiles_m = tiles_over(w.dim, rr::tile_m(tt));
+    w.tiles_n = tiles_over(w.c1 - w.c0, rr::tile_n(tt));
+    const hipError_t e = rr::launch_weight_grad(w, k, tt, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
 rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weights, const void* targets,
                                    int target_bytes, float* loss, float* lse, int p, size_t tokens, size_t dim,
@@ -1463,6 +1513,7 @@ rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weight
     c.x = hidden;
     c.out = ws + pl.pack_x;
     c.out_stride = static_cast<uint64_t>(pl.dim_pad) * pl.esz;
+    c.unit = align_unit({reinterpret_cast<uintptr_t>(hidden)}, dim * pl.esz);
     c.tokens = c.rows = pl.tokens;
     c.dim = pl.dim;
     if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy: copy");
@@ -1475,16 +1526,12 @@ rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weight
   a.part = reinterpret_cast<float*>(ws + pl.part);
   a.hit = reinterpret_cast<float*>(ws + pl.hit);
   a.tokens = pl.tokens;
-  a.tiles_n = tiles_over(tokens, rr::tile_n(pl.logits_tile));
   for (uint32_t c0 = 0; c0 < pl.sh.off[p]; c0 += pl.piece) {
-    a.c0 = c0;
-    a.c1 = std::min(pl.sh.off[p], c0 + pl.piece);
-    if ((e = vocab_piece(pl, sh, pack, k, a.c0, a.c1, ws, a.sh, s)) != hipSuccess)
+    const uint32_t c1 = std::min(pl.sh.off[p], c0 + pl.piece);
+    if ((e = vocab_piece(pl, sh, pack, k, c0, c1, ws, a.sh, s)) != hipSuccess)
       return hip_fail(e, "vocab_cross_entropy: copy");
-    a.tiles_m = tiles_over(a.c1 - a.c0, rr::tile_m(pl.logits_tile));
-    if ((e = rr::launch_logits(a, k, pl.logits_tile, false, s)) != hipSuccess)
+    if ((e = vocab_logits(a, k, pl.logits_tile, false, c0, c1, pl.tokens, s)) != hipSuccess)
       return hip_fail(e, "vocab_cross_entropy: logits");
-    a.tile0 += a.tiles_m;
   }
   rr::LossArgs l;
   l.part = a.part;
@@ -1570,6 +1617,7 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   c.sh = sh;
   c.tcol = tcol;
   c.out_stride = row;
+  c.unit = align_unit({reinterpret_cast<uintptr_t>(hidden)}, dim * pl.esz);
   c.tokens = pl.tokens;
   c.rows = pl.tokens_pad;
   c.dim = pl.dim;
@@ -1602,7 +1650,6 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   a.lo = lo;
   a.tokens = pl.tokens;
   a.grad_rows = pl.tokens_pad;
-  a.tiles_n = tiles_over(pl.tokens_pad, rr::tile_n(pl.logits_tile));
   rr::HiddenGradArgs h;
   memset(&h, 0, sizeof(h));
   h.grad = a.grad;
@@ -1623,7 +1670,6 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   h.grad_loss = grad_loss;
   rr::WeightGradArgs w;
   memset(&w, 0, sizeof(w));
-  w.grad = a.grad;
   w.xg = ws + pl.xg;
   w.xg_stride = row;
   w.scale = f16 ? scale : nullptr;
@@ -1632,7 +1678,6 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
   w.tokens = pl.tokens;
   w.rows = pl.tokens_pad;
   w.dim = pl.dim;
-  w.tiles_m = tiles_over(dim, rr::tile_m(pl.weight_tile));
   w.vec = (dim * esz) % 16 == 0 ? 1 : 0;
   if (dweights)
     for (int r = 0; r < p; ++r) {
@@ -1643,11 +1688,11 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
     const uint32_t c1 = std::min(pl.sh.off[p], c0 + pl.piece);
     if ((e = vocab_piece(pl, sh, pack, k, c0, c1, ws, a.sh, s)) != hipSuccess)
       return hip_fail(e, "vocab_cross_entropy_grad: copy");
-    a.c0 = h.c0 = w.c0 = c0;
-    a.c1 = h.c1 = w.c1 = c1;
+    h.c0 = c0;
+    h.c1 = c1;
     a.ld = h.ld = w.ld = c1 - c0;
-    a.tiles_m = tiles_over(c1 - c0, rr::tile_m(pl.logits_tile));
-    if ((e = rr::launch_logits(a, k, pl.logits_tile, true, s)) != hipSuccess)
+    a.grad = ws + pl.grad;
+    if ((e = vocab_logits(a, k, pl.logits_tile, true, c0, c1, pl.tokens_pad, s)) != hipSuccess)
       return hip_fail(e, "vocab_cross_entropy_grad: logits");
     if (dhidden) {
       h.sh = a.sh;
@@ -1657,8 +1702,8 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
     }
     if (dweights) {
       w.sh = a.sh;
-      w.tiles_n = tiles_over(c1 - c0, rr::tile_n(pl.weight_tile));
-      if ((e = rr::launch_weight_grad(w, k, pl.weight_tile, s)) != hipSuccess)
+      w.grad = ws + pl.grad;
+      if ((e = vocab_weight_grad(w, k, pl.weight_tile, c0, c1, s)) != hipSuccess)
         return hip_fail(e, "vocab_cross_entropy_grad: dweights");
     }
   }

@@ -17,10 +17,23 @@ constexpr uint64_t kGradBytes = 1ull << 30;
 // Copied weight rows of one piece (inputs whose rows are not 16-byte aligned).
 constexpr uint64_t kPackBytes = 64ull << 20;
 constexpr uint32_t kPieceUnit = 256;
+constexpr uint32_t kUnits = 256;  // compute units
 
 uint32_t ceil_div(uint64_t a, uint64_t b) { return static_cast<uint32_t>((a + b - 1) / b); }
 
 }  // namespace
+
+// A grid of large tiles, one on each compute unit, runs in rounds.  A last round
+// that fills less than half of the units is given to small tiles, which spread
+// it over all of them.
+uint32_t tail_start(uint32_t c0, uint32_t c1, uint32_t other_tiles, VocabTile t) {
+  if (t != VocabTile::k256x256) return c1;
+  const uint64_t tiles = static_cast<uint64_t>(ceil_div(c1 - c0, 256)) * other_tiles;
+  const uint64_t rest = tiles % kUnits;
+  if (tiles < kUnits || rest == 0 || 2 * rest >= kUnits) return c1;
+  const uint64_t full = tiles / kUnits * kUnits / other_tiles;  // tiles of this axis in full rounds
+  return std::min<uint64_t>(c1, c0 + full * 256);
+}
 
 void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vocab, rr_dtype_t dt, bool grad,
                 bool pack) {
@@ -51,36 +64,45 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
   // a grid of at most 2^22 workgroups, and 32-bit offsets within a tile
   most = std::min<uint64_t>(most, 1u << 20);
   most = std::min<uint64_t>(most, (1ull << 22) / std::max(1u, ceil_div(tokens, 256)) * 256);
-  most = std::max<uint64_t>(most / kPieceUnit * kPieceUnit, kPieceUnit);
-  pl.pieces = ceil_div(off, most);
-  pl.piece = ceil_div(ceil_div(off, pl.pieces), kPieceUnit) * kPieceUnit;
+  if (most >= off) {
+    pl.piece = off;
+  } else {
+    most = std::max<uint64_t>(most / kPieceUnit * kPieceUnit, kPieceUnit);
+    pl.piece = ceil_div(ceil_div(off, ceil_div(off, most)), kPieceUnit) * kPieceUnit;
+  }
   pl.pieces = ceil_div(off, pl.piece);
 
   // Tiles: the large tile reads least per product, where there are enough of
-  // them for the 256 compute units; few tokens take the narrow one.
-  const uint32_t piece = std::min(pl.piece, off);
+  // them for the compute units; few tokens take the narrow one.
+  const uint32_t piece = pl.piece;
   if (tokens <= 32) {
     pl.logits_tile = pl.hidden_tile = VocabTile::k128x32;
   } else {
-    pl.logits_tile = static_cast<uint64_t>(ceil_div(piece, 256)) * ceil_div(tokens, 256) >= 256 ? VocabTile::k256x256
-                                                                                                  : VocabTile::k128x128;
+    pl.logits_tile = static_cast<uint64_t>(ceil_div(piece, 256)) * ceil_div(tokens, 256) >= kUnits
+                         ? VocabTile::k256x256
+                         : VocabTile::k128x128;
     pl.hidden_tile = static_cast<uint64_t>(ceil_div(dim, 256)) * ceil_div(tokens, 256) >= 64 ? VocabTile::k256x256
                                                                                               : VocabTile::k128x128;
   }
-  pl.weight_tile = static_cast<uint64_t>(ceil_div(dim, 256)) * ceil_div(piece, 256) >= 256 ? VocabTile::k256x256
-                                                                                            : VocabTile::k128x128;
-  // Few tiles of dhidden: K (the vocabulary) is split over enough workgroups to
-  // fill the chip, each with at least 4 steps.
+  // A product over few tokens is all prologue and output: two smaller
+  // workgroups on a compute unit overlap them.
+  pl.weight_tile = tokens >= 512 && static_cast<uint64_t>(ceil_div(dim, 256)) * ceil_div(piece, 256) >= kUnits
+                       ? VocabTile::k256x256
+                       : VocabTile::k128x128;
+  // Few tiles of dhidden: K (the vocabulary) is split over as many workgroups as
+  // run at once, each with at least 4 steps.  Float32 products are bound by the
+  // matrix cores, so one workgroup a compute unit is all that helps.
   const uint64_t htiles = static_cast<uint64_t>(ceil_div(dim, tile_m(pl.hidden_tile))) *
                           ceil_div(std::max(tokens, 1u), tile_n(pl.hidden_tile));
-  const uint32_t want = pl.hidden_tile == VocabTile::k256x256 ? 256 : pl.hidden_tile == VocabTile::k128x128 ? 512 : 1024;
+  const uint32_t want = pl.hidden_tile == VocabTile::k256x256 || dt == RR_FLOAT32 ? kUnits : 2 * kUnits;
   const uint32_t steps = piece / kSlot;
-  uint64_t splits = std::min<uint64_t>(ceil_div(want, htiles), std::max(1u, steps / 4));
-  pl.splits = static_cast<uint32_t>(std::max<uint64_t>(splits, 1));
+  pl.splits = static_cast<uint32_t>(
+      std::max<uint64_t>(std::min<uint64_t>(want / htiles, std::max(1u, steps / 4)), 1));
 
-  for (uint32_t i = 0; i < pl.pieces; ++i) {
-    const uint32_t c0 = i * pl.piece, c1 = std::min(off, c0 + pl.piece);
-    pl.tiles += ceil_div(c1 - c0, tile_m(pl.logits_tile));
+  for (uint32_t c0 = 0; c0 < off; c0 += pl.piece) {
+    const uint32_t c1 = std::min(off, c0 + pl.piece);
+    const uint32_t cm = tail_start(c0, c1, ceil_div(tokens, 256), pl.logits_tile);
+    pl.tiles += ceil_div(cm - c0, tile_m(pl.logits_tile)) + ceil_div(c1 - cm, 128);
   }
 
   uint64_t at = 0;

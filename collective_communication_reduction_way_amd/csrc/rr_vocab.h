@@ -111,6 +111,7 @@ struct PackRowsArgs {
   const int32_t* scale;
   uint32_t* tcol;         // NULL, or the targets' padded columns are written here
   uint64_t out_stride;    // bytes
+  uint32_t unit;          // bytes (16, 8, 4 or 2) that x and its rows are aligned to
   uint32_t tokens, rows;  // rows: written rows, zero from `tokens` on
   uint32_t dim;
   int32_t target_bytes;
@@ -120,6 +121,7 @@ struct PackWeightArgs {
   VocabShards sh;
   void* out;              // row i = padded column c0 + i
   uint64_t out_stride;
+  uint32_t unit;          // as in PackRowsArgs, of all shards
   uint32_t dim;
   uint32_t c0, c1;
 };
@@ -179,6 +181,10 @@ struct VocabPlan {
   // workspace offsets in bytes
   uint64_t part, hit, pack_x, pack_w, xg, grad, acc, tcol, lo, scale, total;
 };
+
+// Where the columns [c0, c1) of a product go over from tiles `t` to 128x128 tiles
+// (c1: nowhere); other_tiles: the 256-wide tiles of the product's other axis.
+uint32_t tail_start(uint32_t c0, uint32_t c1, uint32_t other_tiles, VocabTile t);
 
 // pack: the inputs are copied into aligned rows first.  The sizes must be valid.
 void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vocab, rr_dtype_t dt, bool grad,

@@ -14,33 +14,44 @@ __device__ __forceinline__ bool counts(const void* targets, int bytes, uint32_t 
 }
 
 // lse = log sum exp over the tiles' (maximum, sum) pairs and the loss lse -
-// target logit.  32 threads share a token, 8 tokens a workgroup, so that one
-// token's few hundred tiles are read by many lanes at once and many tokens'
-// pairs still fill whole 64-byte segments.
+// target logit.  P threads share a token, 256 / P tokens a workgroup: 32 where
+// there are many tokens (8 tokens' pairs fill a 64-byte segment), 256 where
+// there are few (one token's few hundred pairs are read at once).
+__device__ __forceinline__ void merge(float& mx, float& sum, float m2, float s2) {
+  const float top = fmaxf(mx, m2);
+  const float ref = top == -__builtin_inff() ? 0.f : top;
+  sum = sum * __expf(mx - ref) + s2 * __expf(m2 - ref);
+  mx = top;
+}
+
+template <int P>
 __global__ __launch_bounds__(256) void k_loss(LossArgs a) {
-  __shared__ float sm[32][8][2];
-  const uint32_t ti = threadIdx.x & 7, part = threadIdx.x >> 3;
-  const uint32_t t = blockIdx.x * 8 + ti;
+  constexpr uint32_t T = 256 / P;
+  __shared__ float sm[P][T][2];
+  const uint32_t ti = threadIdx.x % T, part = threadIdx.x / T;
+  const uint32_t t = blockIdx.x * T + ti;
   float mx = -__builtin_inff(), sum = 0.f;
   if (t < a.tokens) {
-    for (uint32_t i = part; i < a.tiles; i += 32) {
-      const float2 v = *reinterpret_cast<const float2*>(a.part + (static_cast<uint64_t>(i) * a.tokens + t) * 2);
-      const float top = fmaxf(mx, v.x);
-      const float ref = top == -__builtin_inff() ? 0.f : top;
-      sum = sum * __expf(mx - ref) + v.y * __expf(v.x - ref);
-      mx = top;
+    const float2* p = reinterpret_cast<const float2*>(a.part) + t;
+    uint32_t i = part;
+    for (; i + 3 * P < a.tiles; i += 4 * P) {
+      float2 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = p[static_cast<uint64_t>(i + j * P) * a.tokens];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) merge(mx, sum, v[j].x, v[j].y);
+    }
+    for (; i < a.tiles; i += P) {
+      const float2 v = p[static_cast<uint64_t>(i) * a.tokens];
+      merge(mx, sum, v.x, v.y);
     }
   }
   sm[part][ti][0] = mx;
   sm[part][ti][1] = sum;
   __syncthreads();
-  for (uint32_t h = 16; h > 0; h >>= 1) {
+  for (uint32_t h = P / 2; h > 0; h >>= 1) {
     if (part < h) {
-      const float m2 = sm[part + h][ti][0], s2 = sm[part + h][ti][1];
-      const float top = fmaxf(mx, m2);
-      const float ref = top == -__builtin_inff() ? 0.f : top;
-      sum = sum * __expf(mx - ref) + s2 * __expf(m2 - ref);
-      mx = top;
+      merge(mx, sum, sm[part + h][ti][0], sm[part + h][ti][1]);
       sm[part][ti][0] = mx;
       sm[part][ti][1] = sum;
     }
@@ -72,12 +83,20 @@ __global__ __launch_bounds__(1024) void k_grad_scale(const float* g, const void*
   }
 }
 
-// 16 bytes of a row from element d on, zeros from `dim` on.
+// 16 bytes of a row from element d on, zeros from `dim` on; in loads of `unit`
+// bytes where the row goes on that far.
 template <class S>
-__device__ __forceinline__ void read_chunk(const S* row, uint32_t d, uint32_t dim, bool vec, S* out) {
+__device__ __forceinline__ void read_chunk(const S* row, uint32_t d, uint32_t dim, uint32_t unit, S* out) {
   constexpr uint32_t EPC = 16 / sizeof(S);
-  if (vec) {
+  const bool whole = d + EPC <= dim;
+  if (whole && unit == 16) {
     *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(row + d);
+  } else if (whole && unit == 8) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) reinterpret_cast<uint2*>(out)[j] = reinterpret_cast<const uint2*>(row + d)[j];
+  } else if (whole && unit == 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(out)[j] = reinterpret_cast<const uint32_t*>(row + d)[j];
   } else {
 #pragma unroll
     for (uint32_t j = 0; j < EPC; ++j) out[j] = d + j < dim ? row[d + j] : S(0);
@@ -103,12 +122,11 @@ __global__ __launch_bounds__(256) void k_pack_rows(PackRowsArgs a) {
     f = g == 0.f ? 0.f : fabsf(g) < __builtin_inff() ? ldexpf(1.f, token_exponent(g) - a.scale[0]) : 1.f;
   }
   const S* row = static_cast<const S*>(a.x) + static_cast<uint64_t>(t) * a.dim;
-  const bool vec = a.dim % EPC == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0;
   char* out = static_cast<char*>(a.out) + t * a.out_stride;
   for (uint32_t d = threadIdx.x * EPC; d < a.dim; d += 256 * EPC) {
     __attribute__((aligned(16))) S v[EPC];
     if (live) {
-      read_chunk<S>(row, d, a.dim, vec, v);
+      read_chunk<S>(row, d, a.dim, a.unit, v);
     } else {
 #pragma unroll
       for (uint32_t j = 0; j < EPC; ++j) v[j] = S(0);
@@ -135,7 +153,7 @@ __global__ __launch_bounds__(256) void k_pack_weight(PackWeightArgs a) {
   for (uint32_t d = threadIdx.x * EPC; d < a.dim; d += 256 * EPC) {
     __attribute__((aligned(16))) S v[EPC];
     if (row) {
-      read_chunk<S>(row, d, a.dim, false, v);
+      read_chunk<S>(row, d, a.dim, a.unit, v);
     } else {
 #pragma unroll
       for (uint32_t j = 0; j < EPC; ++j) v[j] = S(0);
@@ -210,7 +228,10 @@ void run_join(const JoinArgs& a, hipStream_t s) {
 
 hipError_t launch_loss(const LossArgs& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_loss, dim3((a.tokens + 7) / 8), dim3(256), 0, s, a);
+  if (a.tokens < 256)
+    hipLaunchKernelGGL(k_loss<256>, dim3(a.tokens), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(k_loss<32>, dim3((a.tokens + 7) / 8), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
