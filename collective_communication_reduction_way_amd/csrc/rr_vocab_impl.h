@@ -381,6 +381,22 @@ __device__ __forceinline__ void wait_for_all_but() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// The loads of the first two steps.
+template <class T, class LA, class LB>
+__device__ __forceinline__ void k_start(char* lds, LA& la, LB& lb) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    la.prepare();
+#pragma unroll
+    for (int q = 0; q < LA::NQ; ++q) la.load(q, lds + i * T::ABYTES);
+#pragma unroll
+    for (int q = 0; q < LB::NQ; ++q) lb.load(q, lds + T::BOFF + i * T::BBYTES);
+    la.advance();
+    lb.advance();
+  }
+}
+
+// After k_start.  Until here the third slot of A, lds + 2 ABYTES, is free.
 template <class E, class T, class LA, class LB, class FA, class FB>
 __device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x16_t (&acc)[T::MT][T::NT], LA& la, LB& lb, FA fa,
                                        FB fb) {
@@ -391,23 +407,17 @@ __device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x16_t (&acc
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = f32x16_t{};
-  if (steps == 0) return;
+  if (steps == 0) {  // (the loads of k_start read zeros)
+    wait_for_loads();
+    __syncthreads();
+    return;
+  }
   Frag<E> a[2][MT], b[2][NT];
   const auto read = [&](int to, int i, const char* ta, const char* tb, int s) __attribute__((always_inline)) {
     if (i < NT) b[to][i] = fb(tb, i, s);
     else if (i < NT + MT) a[to][i - NT] = fa(ta, i - NT, s);
   };
   char* const lds_b = lds + T::BOFF;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    la.prepare();
-#pragma unroll
-    for (int q = 0; q < LA::NQ; ++q) la.load(q, lds + i * T::ABYTES);
-#pragma unroll
-    for (int q = 0; q < LB::NQ; ++q) lb.load(q, lds_b + i * T::BBYTES);
-    la.advance();
-    lb.advance();
-  }
   wait_for_all_but<LA::NQ + LB::NQ>();
   meet();
 #pragma unroll
@@ -494,15 +504,29 @@ __device__ __forceinline__ void put16(char* lds, uint32_t n, uint32_t m, const f
   *reinterpret_cast<uint2*>(lds + n * kRow16<T> + m * 2) = make_uint2(w0 & mask, w1 & mask);
 }
 
-// out(n, m): where the 8 values from m on of row n go, or NULL.
-template <class E, class T, class OUT>
-__device__ __forceinline__ void take16(const char* lds, OUT out) {
-  constexpr uint32_t kChunks = T::BM / 8, kRows = kWaves * 64 / kChunks;
-  const uint32_t c = threadIdx.x % kChunks;
-#pragma unroll 4
-  for (uint32_t n = threadIdx.x / kChunks; n < T::BN; n += kRows) {
-    char* q = out(n, c * 8);
-    if (q) *reinterpret_cast<u32x4*>(q) = *reinterpret_cast<const u32x4*>(lds + n * kRow16<T> + c * 16);
+// Rows of the tile in runs of up to 64: slot(i) says where run i goes (`rows` of
+// them exist); `cols` values of a row exist, a multiple of 8.
+struct OutRows {
+  char* base;
+  uint64_t stride;  // bytes
+  uint32_t rows;
+};
+template <class E, class T, class SLOT>
+__device__ __forceinline__ void take16(const char* lds, uint32_t cols, SLOT slot) {
+  constexpr uint32_t kChunks = T::BM / 8, kRows = kWaves * 64 / kChunks, kRun = T::BN < 64 ? T::BN : 64;
+  const uint32_t c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+#pragma unroll
+  for (uint32_t i = 0; i < T::BN / kRun; ++i) {
+    const OutRows o = slot(i);
+    const uint32_t rows = c * 8 < cols ? o.rows : 0;
+    char* const q = o.base + c * 16;
+    u32x4 v[kRun / kRows];
+#pragma unroll
+    for (uint32_t j = 0; j < kRun / kRows; ++j)
+      v[j] = *reinterpret_cast<const u32x4*>(lds + (i * kRun + r0 + j * kRows) * kRow16<T> + c * 16);
+#pragma unroll
+    for (uint32_t j = 0; j < kRun / kRows; ++j)
+      if (r0 + j * kRows < rows) *reinterpret_cast<u32x4*>(q + (r0 + j * kRows) * o.stride) = v[j];
   }
 }
 
@@ -523,6 +547,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
   KcLoader<T::BN> lb;
   la.init(a.sh, a.w_stride, cbase, a.c1, a.kbytes, wave, lane);
   lb.init(a.x, a.x_stride, t0, a.tokens, a.kbytes, 0, wave, lane);
+  k_start<T>(lds, la, lb);
   f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
   const int m0 = wm * (T::MT * 32), n0 = wn * (T::NT * 32);
@@ -668,10 +693,10 @@ __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
     }
     if constexpr (sizeof(S) == 2) {
       __syncthreads();
-      take16<E, T>(lds, [&](uint32_t row, uint32_t m) -> char* {
-        const uint32_t t = t0 + row, c = cbase + m;
-        return t < a.grad_rows && c < a.c1 ? reinterpret_cast<char*>(static_cast<S*>(a.grad) + t * a.ld + (c - a.c0))
-                                           : nullptr;
+      take16<E, T>(lds, a.c1 - cbase, [&](uint32_t i) {
+        const uint32_t t = t0 + i * 64;
+        return OutRows{reinterpret_cast<char*>(static_cast<S*>(a.grad) + t * a.ld + (cbase - a.c0)), a.ld * sizeof(S),
+                       t < a.grad_rows ? a.grad_rows - t : 0};
       });
     }
   }
@@ -700,6 +725,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_hidden_grad(HiddenGradArgs a) {
   la.init(a.sh, a.w_stride, static_cast<uint64_t>(d0) * esz, static_cast<uint64_t>(a.dim - d0) * esz,
           a.c0 + k_lo * Frag<E>::kBK, a.c0 + k_hi * Frag<E>::kBK, wave, lane);
   lb.init(a.grad, a.ld * esz, t0, a.grad_rows, (a.c1 - a.c0) * esz, k_lo, wave, lane);
+  k_start<T>(lds, la, lb);
   f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
   const int m0 = wm * (T::MT * 32), n0 = wn * (T::NT * 32);
@@ -733,11 +759,10 @@ __global__ __launch_bounds__(kWaves * 64) void k_hidden_grad(HiddenGradArgs a) {
     }
     if constexpr (esz == 2) {
       __syncthreads();
-      take16<E, T>(lds, [&](uint32_t n, uint32_t m) -> char* {
-        const uint32_t t = t0 + n, d = d0 + m;
-        return t < a.tokens && d < a.dim
-                   ? reinterpret_cast<char*>(static_cast<S*>(a.out) + static_cast<uint64_t>(t) * a.dim + d)
-                   : nullptr;
+      take16<E, T>(lds, a.dim - d0, [&](uint32_t i) {
+        const uint32_t t = t0 + i * 64;
+        return OutRows{reinterpret_cast<char*>(static_cast<S*>(a.out) + static_cast<uint64_t>(t) * a.dim + d0),
+                       static_cast<uint64_t>(a.dim) * sizeof(S), t < a.tokens ? a.tokens - t : 0};
       });
     }
     return;
@@ -773,6 +798,41 @@ __global__ __launch_bounds__(kWaves * 64) void k_hidden_grad(HiddenGradArgs a) {
   }
 }
 
+// The tokens of [b, b + kScan) whose target's padded column lies in [first, first +
+// n) join `list`, which holds `have`, always in the same order.  The list takes
+// 64 + kScan entries and 16 bytes more.
+constexpr uint32_t kScan = 8 * kWaves * 64;
+
+__device__ __forceinline__ void scan_targets(const uint32_t* tcol, uint32_t tokens, uint32_t b, uint32_t first,
+                                             uint32_t n, uint32_t* list, uint32_t& have) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t* const found = list + 64 + kScan;
+  uint64_t mask[8];
+  uint32_t count = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t t = b + j * kWaves * 64 + threadIdx.x;
+    const uint32_t c = t < tokens ? tcol[t] : kMasked;
+    mask[j] = __ballot(c - first < n);  // kMasked - first is out of range
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) count += __popcll(mask[j]);
+  if (lane == 0) found[wave] = count;
+  __syncthreads();
+  uint32_t at = have;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) at += found[w];
+    have += found[w];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (mask[j] >> lane & 1) list[at + __popcll(mask[j] & ((1ull << lane) - 1))] = b + j * kWaves * 64 + threadIdx.x;
+    at += __popcll(mask[j]);
+  }
+  __syncthreads();
+}
+
 // ---------------------------------------------------------------------------
 // dweights: M = dim, N = the piece's padded columns, K = tokens.
 template <class E, class T>
@@ -792,6 +852,19 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
   la.init(xg, a.xg_stride, xg_cols, a.rows / Frag<E>::kBK, wave, lane);
   lb.init(static_cast<const char*>(a.grad) + static_cast<uint64_t>(v0) * esz, a.ld * esz,
           static_cast<uint64_t>(a.c1 - a.c0 - v0) * esz, a.rows / Frag<E>::kBK, wave, lane);
+  k_start<T>(lds, la, lb);
+  // What rounding took from the targets' entries (16-bit types): the tokens
+  // whose target lies in this tile's columns are added as further K steps of
+  // 64.  There are few, since the whole vocabulary shares the tokens: they are
+  // looked up while the first loads arrive, and kept one a lane.
+  const uint32_t first = a.c0 + v0;
+  uint32_t hits = 0, mine = 0;
+  if constexpr (esz == 2) {
+    uint32_t* const list = reinterpret_cast<uint32_t*>(lds + 2 * T::ABYTES);
+    for (uint32_t b = 0; b < a.tokens && hits <= 64; b += kScan)
+      scan_targets(a.tcol, a.tokens, b, first, T::BN, list, hits);
+    if (lane < hits && hits <= 64) mine = list[lane];
+  }
   f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
   const int m0 = wm * (T::MT * 32), n0 = wn * (T::NT * 32);
@@ -800,13 +873,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
       [&](const char* t, int m, int s) { return frag_ks<E, T::BM>(t, m0 + m * 32, s, lane); },
       [&](const char* t, int n, int s) { return frag_ks<E, T::BN>(t, n0 + n * 32, s, lane); });
   if constexpr (esz == 2) {
-    // What rounding took from the targets' entries: the tokens whose target
-    // lies in this tile (few: the whole vocabulary shares the tokens) are
-    // listed in order and added as further K steps of 64.
-    uint32_t* const list = reinterpret_cast<uint32_t*>(lds + T::ABYTES);  // 64 + kWaves * 64
-    uint32_t* const found = list + 64 + kWaves * 64;
-    const uint32_t first = a.c0 + v0;
-    uint32_t have = 0;
+    uint32_t* const list = reinterpret_cast<uint32_t*>(lds + T::ABYTES);
     const auto add = [&](uint32_t n) {
       // rows of different tokens: the list's row k, this lane's chunk
       constexpr uint32_t RB = T::BM * esz;
@@ -840,32 +907,28 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
       }
       __syncthreads();
     };
-    for (uint32_t b = 0; b < a.tokens; b += kWaves * 64) {
-      const uint32_t t = b + threadIdx.x;
-      const bool in = t < a.tokens && a.tcol[t] - first < T::BN;  // kMasked - first is out of range
-      const uint64_t mask = __ballot(in);
-      if (lane == 0) found[wave] = __popcll(mask);
-      __syncthreads();
-      uint32_t at = have, total = have;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        if (w < wave) at += found[w];
-        total += found[w];
+    // the list at hand, or, where it was too long, all of it again, 64 at a time
+    uint32_t have = hits <= 64 ? hits : 0, b = hits <= 64 ? a.tokens : 0;
+    if (wave == 0) list[lane] = mine;
+    __syncthreads();
+    for (;;) {
+      while (have < 64 && b < a.tokens) {
+        scan_targets(a.tcol, a.tokens, b, first, T::BN, list, have);
+        b += kScan;
       }
-      if (in) list[at + __popcll(mask & ((1ull << lane) - 1))] = t;
-      have = total;
-      __syncthreads();
-      while (have >= 64) {
-        add(64);
-        const uint32_t left = have - 64;  // at most NW * 64 - 1
-        const uint32_t v = threadIdx.x < left ? list[64 + threadIdx.x] : 0;
+      if (have == 0) break;
+      const uint32_t n = have < 64 ? have : 64;
+      add(n);
+      have -= n;
+      // the rest moves to the front, a workgroup's width at a time
+      for (uint32_t i = 0; i < have; i += kWaves * 64) {
+        const uint32_t k = i + threadIdx.x;
+        const uint32_t v = k < have ? list[64 + k] : 0;
         __syncthreads();
-        if (threadIdx.x < left) list[threadIdx.x] = v;
+        if (k < have) list[k] = v;
         __syncthreads();
-        have = left;
       }
     }
-    if (have > 0) add(have);
   }
   float scale = 1.f;
   if constexpr (__is_same(E, EF16)) scale = ldexpf(1.f, a.scale[0] - 15);
@@ -893,9 +956,14 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
             put16<E, T>(lds, n0 + n * 32 + (lane & 31), m0 + m * 32 + i * 8 + (lane >> 5) * 4, v, ~0u);
         }
     __syncthreads();
-    take16<E, T>(lds, [&](uint32_t n, uint32_t m) -> char* {
-      S* row = d0 + m < a.dim ? row_of(n) : nullptr;
-      return row ? reinterpret_cast<char*>(row + d0 + m) : nullptr;
+    int r = 0;
+    take16<E, T>(lds, a.dim - d0, [&](uint32_t i) {
+      const uint32_t c = a.c0 + v0 + i * 64;  // a slot: rows of one shard
+      if (c >= a.c1) return OutRows{nullptr, 0, 0};
+      while (c >= a.sh.off[r + 1]) ++r;
+      const uint32_t local = c - a.sh.off[r];
+      return OutRows{reinterpret_cast<char*>(static_cast<S*>(a.dw[r]) + static_cast<uint64_t>(local) * a.dim + d0),
+                     static_cast<uint64_t>(a.dim) * sizeof(S), a.sh.rows[r] > local ? a.sh.rows[r] - local : 0};
     });
     return;
   }
