@@ -496,20 +496,43 @@ def _drop(drop, seed, offset, offset_dev, device):
     return _Dropout(float(drop), int(seed) & mask, int(offset) & mask, ptr)
 
 
-def _residuals(residuals, outs, what):
-    """The residual pointers (or None): a list of p tensors, or a 2-D tensor."""
-    if residuals is None:
-        return None
-    res = _ranks(residuals, f"{what} residuals")
-    if len(res) != len(outs) or any(a.numel() != o.numel() for a, o in zip(res, outs)) or (
-            res[0].dtype != outs[0].dtype or res[0].device != outs[0].device):
-        raise ValueError(f"{what}: residuals must match the outputs in count, length, dtype and device")
-    return _ptr_array([t.data_ptr() for t in res])
+def _rank_ptrs(bufs, what):
+    """Rank buffers of equal length -> (pointers, count, length, a tensor of
+    theirs); a 2-D tensor without building a view for every row."""
+    import torch
+
+    if isinstance(bufs, torch.Tensor) and bufs.dim() == 2 and bufs.shape[0] > 0 and bufs.is_contiguous():
+        p, n = bufs.shape
+        base, step = bufs.data_ptr(), n * bufs.element_size()
+        return (ctypes.c_void_p * p)(*range(base, base + p * step, step) if step else [base] * p), p, n, bufs
+    bufs = _ranks(bufs, what)
+    n = bufs[0].numel()
+    if any(t.numel() != n for t in bufs):
+        raise ValueError(f"{what}: rank buffers must have equal length")
+    return _ptr_array([t.data_ptr() for t in bufs]), len(bufs), n, bufs[0]
 
 
-def _same_place(a, b, what):
-    if a.dtype != b.dtype or a.device != b.device:
+def _dropout_call(func, what, ins, outs, residuals, drop, seed, offset, offset_dev, stream, shard_in=False,
+                  shard_out=False):
+    send, p, n_in, x = _rank_ptrs(ins, f"{what} inputs")
+    recv, q, n_out, y = (send, p, n_in, x) if outs is None else _rank_ptrs(outs, f"{what} outputs")
+    n = n_out if shard_in else n_in
+    if q != p or n_in * (p if shard_in else 1) != n or n_out * (p if shard_out else 1) != n:
+        lengths = "p inputs of n/p and p outputs of n" if shard_in else (
+            "p inputs of n and p outputs of n/p" if shard_out else "p inputs and p outputs of n")
+        raise ValueError(f"{what}: need {lengths} elements")
+    if y.dtype != x.dtype or y.device != x.device:
         raise ValueError(f"{what}: inputs and outputs must share device and dtype")
+    args = [send, recv, p, n, _dtype_code(x), _drop(drop, seed, offset, offset_dev, x.device), _stream(x, stream)]
+    if not shard_in:
+        res = None
+        if residuals is not None:
+            res, q, n_res, z = _rank_ptrs(residuals, f"{what} residuals")
+            if q != p or n_res != n_out or z.dtype != y.dtype or z.device != y.device:
+                raise ValueError(f"{what}: residuals must match the outputs in count, length, dtype and device")
+        args.insert(1, res)
+    _check(getattr(lib(), func)(*args), func)
+    return ins if outs is None else outs
 
 
 def all_reduce_dropout(ins, outs=None, drop=0.1, seed=0, offset=0, residuals=None, offset_dev=None, stream=None):
@@ -523,69 +546,28 @@ def all_reduce_dropout(ins, outs=None, drop=0.1, seed=0, offset=0, residuals=Non
     of the inputs: ``dropout`` of each rank's output gradient with the same
     (seed, offset), where the ranks hold copies of one loss.
     """
-    ins = _ranks(ins, "all_reduce_dropout inputs")
-    outs = ins if outs is None else _ranks(outs, "all_reduce_dropout outputs")
-    p, n = len(ins), ins[0].numel()
-    _same_place(ins[0], outs[0], "all_reduce_dropout")
-    if len(outs) != p or any(t.numel() != n for t in ins + outs):
-        raise ValueError("all_reduce_dropout: need p inputs and p outputs of equal length")
-    res = _residuals(residuals, outs, "all_reduce_dropout")
-    st = lib().rr_all_reduce_dropout(_ptr_array([t.data_ptr() for t in ins]), res,
-                                     _ptr_array([t.data_ptr() for t in outs]), p, n, _dtype_code(ins[0]),
-                                     _drop(drop, seed, offset, offset_dev, ins[0].device), _stream(ins[0], stream))
-    _check(st, "rr_all_reduce_dropout")
-    return outs
+    return _dropout_call("rr_all_reduce_dropout", "all_reduce_dropout", ins, outs, residuals, drop, seed, offset,
+                         offset_dev, stream)
 
 
 def reduce_scatter_dropout(ins, outs, drop=0.1, seed=0, offset=0, residuals=None, offset_dev=None, stream=None):
     """Rank c's output (n/p elements) becomes its residual plus chunk c of the
     dropped-out sum.  Gradient of the inputs: ``all_gather_dropout``."""
-    ins = _ranks(ins, "reduce_scatter_dropout inputs")
-    outs = _ranks(outs, "reduce_scatter_dropout outputs")
-    p, n = len(ins), ins[0].numel()
-    _same_place(ins[0], outs[0], "reduce_scatter_dropout")
-    if len(outs) != p or any(t.numel() != n for t in ins) or any(o.numel() * p != n for o in outs):
-        raise ValueError("reduce_scatter_dropout: need p inputs of n and p outputs of n/p elements")
-    res = _residuals(residuals, outs, "reduce_scatter_dropout")
-    st = lib().rr_reduce_scatter_dropout(_ptr_array([t.data_ptr() for t in ins]), res,
-                                         _ptr_array([t.data_ptr() for t in outs]), p, n, _dtype_code(ins[0]),
-                                         _drop(drop, seed, offset, offset_dev, ins[0].device),
-                                         _stream(ins[0], stream))
-    _check(st, "rr_reduce_scatter_dropout")
-    return outs
+    return _dropout_call("rr_reduce_scatter_dropout", "reduce_scatter_dropout", ins, outs, residuals, drop, seed,
+                         offset, offset_dev, stream, shard_out=True)
 
 
 def dropout(ins, outs=None, drop=0.1, seed=0, offset=0, residuals=None, offset_dev=None, stream=None):
     """Every rank's output becomes its residual plus its own dropped-out input
     (outs=None: in place), one mask for all ranks."""
-    ins = _ranks(ins, "dropout inputs")
-    outs = ins if outs is None else _ranks(outs, "dropout outputs")
-    p, n = len(ins), ins[0].numel()
-    _same_place(ins[0], outs[0], "dropout")
-    if len(outs) != p or any(t.numel() != n for t in ins + outs):
-        raise ValueError("dropout: need p inputs and p outputs of equal length")
-    res = _residuals(residuals, outs, "dropout")
-    st = lib().rr_dropout(_ptr_array([t.data_ptr() for t in ins]), res, _ptr_array([t.data_ptr() for t in outs]), p,
-                          n, _dtype_code(ins[0]), _drop(drop, seed, offset, offset_dev, ins[0].device),
-                          _stream(ins[0], stream))
-    _check(st, "rr_dropout")
-    return outs
+    return _dropout_call("rr_dropout", "dropout", ins, outs, residuals, drop, seed, offset, offset_dev, stream)
 
 
 def all_gather_dropout(ins, outs, drop=0.1, seed=0, offset=0, offset_dev=None, stream=None):
     """Every rank's output (n elements) becomes the dropped-out concatenation of
     the p shards."""
-    ins = _ranks(ins, "all_gather_dropout inputs")
-    outs = _ranks(outs, "all_gather_dropout outputs")
-    p, n = len(ins), outs[0].numel()
-    _same_place(ins[0], outs[0], "all_gather_dropout")
-    if len(outs) != p or any(o.numel() != n for o in outs) or any(i.numel() * p != n for i in ins):
-        raise ValueError("all_gather_dropout: need p shards of n/p elements and p outputs of n")
-    st = lib().rr_all_gather_dropout(_ptr_array([t.data_ptr() for t in ins]),
-                                     _ptr_array([t.data_ptr() for t in outs]), p, n, _dtype_code(ins[0]),
-                                     _drop(drop, seed, offset, offset_dev, ins[0].device), _stream(ins[0], stream))
-    _check(st, "rr_all_gather_dropout")
-    return outs
+    return _dropout_call("rr_all_gather_dropout", "all_gather_dropout", ins, outs, None, drop, seed, offset,
+                         offset_dev, stream, shard_in=True)
 
 
 def vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, dtype, grad=False):

@@ -1241,17 +1241,15 @@ static rr_status_t run_dropout(const char* what, rr::DropForm form, const void* 
   if (n == 0) return ok();
   const bool shard_in = form == rr::DropForm::kGather, shard_out = form == rr::DropForm::kScatter;
   std::vector<Range> outs, ins;
-  bool vec = true, one = true;
+  bool one = true;
   for (int r = 0; r < p; ++r) {
     a.in[r] = send[r];
     a.out[r] = recv[r];
-    vec = vec && aligned16(send[r]) && aligned16(recv[r]);
     outs.push_back(range_of(recv[r], out_len * esz, r));
     ins.push_back(range_of(send[r], in_len * esz, r));
     if (!residuals) continue;
     if ((st = check_buf(residuals[r], esz, "residuals", r))) return st;
     a.res[r] = residuals[r];
-    vec = vec && aligned16(residuals[r]);
     one = one && residuals[r] == residuals[0];
   }
   // In place: a rank's output may be its own input (the chunk's slot on a
@@ -1281,12 +1279,9 @@ static rr_status_t run_dropout(const char* what, rr::DropForm form, const void* 
     a.chunks = p;
     rr::chunk_bounds(p, n, a.bound);
   }
-  // a sharded side's groups must start on its 16-byte boundaries
-  if ((shard_in || shard_out) && ((n / p) * esz) % 16) vec = false;
-  a.vec = vec ? 1 : 0;
   const Tuning& t = tuning();
   if (t.log)
-    fprintf(stderr, "[rr] %s: p=%d n=%zu vec=%d residuals=%d\n", what, p, n, a.vec, a.has_res ? (a.one_res ? 1 : p) : 0);
+    fprintf(stderr, "[rr] %s: p=%d n=%zu residuals=%d\n", what, p, n, a.has_res ? (a.one_res ? 1 : p) : 0);
   const hipError_t e = rr::launch_dropout(a, form, kind_of(dtype), reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, what);
   return ok();

@@ -252,7 +252,6 @@ struct DropArgs {
   int32_t chunks;
   int32_t has_res;
   int32_t one_res;                   // every res[r] is the same buffer
-  int32_t vec;                       // 1: 16-byte accesses
 };
 
 hipError_t launch_dropout(const DropArgs& a, DropForm f, Kind k, hipStream_t stream);
