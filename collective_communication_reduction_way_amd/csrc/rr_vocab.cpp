@@ -72,32 +72,35 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
   }
   pl.pieces = ceil_div(off, pl.piece);
 
-  // Tiles: the large tile reads least per product, where there are enough of
-  // them for the compute units; few tokens take the narrow one.
-  const uint32_t piece = pl.piece;
+  // Tiles.  Up to 32 tokens take the narrow one.  The large tile reads least per
+  // product, but only one workgroup fits on a compute unit, so nothing
+  // overlaps its first loads and its output: it needs enough tiles for the
+  // units, and enough steps of K in each.  Measured in bfloat16 on cold caches
+  // (tokens x dim x vocabulary: large / small tile, us):
+  //   logits, by the tiles: 1024 x 4096 x 32000 (500 tiles) 233 / 298; 256 x 4096
+  //     x 32000 (125) 128 / 118; 512 x 768 x 50257 (394) 71 / 72;
+  //   dhidden, by the steps over all tiles: 2048 x 768 x 50257 (18840) 416 / 435;
+  //     4096 x 512 x 32000 (16000) 395 / 413; 512 x 768 x 50257 (4710) 174 / 162;
+  //     1024 x 1024 x 8000 (2000) 102 / 71;
+  //   dweights, by the tokens: 2048 x 768 x 50257 422 / 435; 4096 x 512 x 32000 354 /
+  //     398; 1024 x 4096 x 32000 613 / 587; 512 x 2048 x 16000 133 / 110.
+  const uint32_t piece = pl.piece, steps = piece / kSlot;
+  const uint64_t tt = ceil_div(tokens, 256), dd = ceil_div(dim, 256), vv = ceil_div(piece, 256);
+  const auto pick = [](bool large) { return large ? VocabTile::k256x256 : VocabTile::k128x128; };
   if (tokens <= 32) {
     pl.logits_tile = pl.hidden_tile = VocabTile::k128x32;
   } else {
-    pl.logits_tile = static_cast<uint64_t>(ceil_div(piece, 256)) * ceil_div(tokens, 256) >= kUnits
-                         ? VocabTile::k256x256
-                         : VocabTile::k128x128;
-    pl.hidden_tile = static_cast<uint64_t>(ceil_div(dim, 256)) * ceil_div(tokens, 256) >= 64 ? VocabTile::k256x256
-                                                                                              : VocabTile::k128x128;
+    pl.logits_tile = pick(vv * tt >= kUnits);
+    pl.hidden_tile = pick(dd * tt * steps >= 32 * kUnits);
   }
-  // A product over few tokens is all prologue and output: two smaller
-  // workgroups on a compute unit overlap them.
-  pl.weight_tile = tokens >= 512 && static_cast<uint64_t>(ceil_div(dim, 256)) * ceil_div(piece, 256) >= kUnits
-                       ? VocabTile::k256x256
-                       : VocabTile::k128x128;
-  // Few tiles of dhidden: K (the vocabulary) is split over as many workgroups as
-  // run at once, each with at least 4 steps.  Float32 products are bound by the
-  // matrix cores, so one workgroup a compute unit is all that helps.
+  pl.weight_tile = pick(tokens >= 2048 && dd * vv >= kUnits * 3 / 4);
+  // Few tiles of dhidden: K (the vocabulary) is split over one workgroup a unit,
+  // each with at least 4 steps.  (Two a unit: 256 x 1024 x 16000 62 instead of 55
+  // us, 96 x 768 x 50257 83 instead of 78, 256 x 4096 x 32000 235 instead of 238.)
   const uint64_t htiles = static_cast<uint64_t>(ceil_div(dim, tile_m(pl.hidden_tile))) *
                           ceil_div(std::max(tokens, 1u), tile_n(pl.hidden_tile));
-  const uint32_t want = pl.hidden_tile == VocabTile::k256x256 || dt == RR_FLOAT32 ? kUnits : 2 * kUnits;
-  const uint32_t steps = piece / kSlot;
   pl.splits = static_cast<uint32_t>(
-      std::max<uint64_t>(std::min<uint64_t>(want / htiles, std::max(1u, steps / 4)), 1));
+      std::max<uint64_t>(std::min<uint64_t>(kUnits / htiles, std::max(1u, steps / 4)), 1));
 
   for (uint32_t c0 = 0; c0 < off; c0 += pl.piece) {
     const uint32_t c1 = std::min(off, c0 + pl.piece);

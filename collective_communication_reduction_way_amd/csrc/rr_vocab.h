@@ -32,7 +32,7 @@ struct VocabShards {
 enum class VocabTile : int { k256x256 = 0, k128x128 = 1, k128x32 = 2 };
 constexpr uint32_t tile_m(VocabTile t) { return t == VocabTile::k256x256 ? 256 : 128; }
 constexpr uint32_t tile_n(VocabTile t) {
-  return t == VocabTile::k256x256 ? 256 : t == VocabTile::k128x128 ? 128 : 32;
+  return t == VocabTile::k256x256 ? 256 : t == VocabTile::k128x32 ? 32 : 128;
 }
 
 // Logits of a piece [c0, c1) of the padded vocabulary.  Forward: the running

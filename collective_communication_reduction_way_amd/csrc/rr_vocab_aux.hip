@@ -174,10 +174,9 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
   const uint32_t t = blockIdx.x;
   const uint32_t c = threadIdx.x % (256 / G), g = threadIdx.x / (256 / G);
   const uint32_t d = blockIdx.y * kCols + c * V;
-  const HiddenRow<E> h(a.sh, a.tcol, a.lo, a.grad_loss, t, a.tokens, a.dim);
   const uint64_t at = static_cast<uint64_t>(t) * a.dim + d;
   float v[V] = {};
-  if (h.live && d < a.dim) {
+  if (d < a.dim) {
     const float* p = a.acc + at;
     const uint32_t lo = a.splits * g / G, hi = a.splits * (g + 1) / G;
 #pragma unroll 8
@@ -203,6 +202,7 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] += part[q][c * V + j];
   }
+  const HiddenRow<E> h(a.sh, a.tcol, a.lo, a.grad_loss, t, a.tokens, a.dim);
   S* out = static_cast<S*>(a.out) + at;
 #pragma unroll
   for (int j = 0; j < V; ++j) {

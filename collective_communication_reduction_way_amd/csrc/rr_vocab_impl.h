@@ -163,6 +163,34 @@ __device__ __forceinline__ uint32_t ks_chunk(uint32_t k, uint32_t pos) {
 // bits (a tile's 256 rows span less than 2^31 bytes), the bases advance.
 constexpr int kWaves = 4;
 
+// Where a KC operand stands in its rows: steps of 128 bytes from `first` on, round
+// to the row's start and up to `first` again, `steps` in all.
+struct RowWalk {
+  uint32_t pos, end, steps;  // bytes; the row's bytes in whole steps; steps left
+  __device__ __forceinline__ void init(uint32_t first, uint32_t steps_all, uint32_t steps_) {
+    pos = first * 128;
+    end = steps_all * 128;
+    steps = steps_;
+  }
+  __device__ __forceinline__ void start(Span& m) const {
+    m.base += pos;
+    m.bytes = m.bytes && steps ? m.bytes - pos : 0;
+  }
+  // The bytes to the next step (negative round the end).
+  __device__ __forceinline__ int32_t advance() {
+    const bool wrap = pos + 128 == end;
+    const int32_t d = wrap ? 128 - static_cast<int32_t>(end) : 128;
+    pos += d;
+    steps -= steps ? 1 : 0;
+    return d;
+  }
+  // Nothing is read after the last step.
+  __device__ __forceinline__ void move(Span& m, int32_t d) const {
+    m.base += d;
+    m.bytes = m.bytes && steps ? m.bytes - d : 0;
+  }
+};
+
 // KC over rows at a constant stride: rows row0 .. of a matrix of `rows` rows.
 template <int R>
 struct KcLoader {
@@ -170,17 +198,19 @@ struct KcLoader {
   uint32_t off[NQ];
   uint32_t left;  // bytes of a row from the lane's chunk on
   Span m;
+  RowWalk w;
   int wave;
 
   __device__ __forceinline__ void init(const void* src, uint64_t stride, uint32_t row0, uint32_t rows, uint32_t kbytes,
-                                       uint32_t kt, int wave_, int lane) {
+                                       uint32_t first, uint32_t steps, int wave_, int lane) {
     wave = wave_;
     const uint32_t chunk = kc_chunk(wave * 8 + (lane >> 3), lane & 7) * 16;
-    const uint32_t skip = kt * 128;
-    left = kbytes > chunk + skip ? kbytes - chunk - skip : 0;
+    left = kbytes > chunk ? kbytes - chunk : 0;
     const uint32_t n = row0 < rows ? (rows - row0 < R ? rows - row0 : R) : 0;
-    m.base = uniform(static_cast<const char*>(src) + row0 * stride + skip);
-    m.bytes = n ? n * static_cast<uint32_t>(stride) - skip : 0;
+    m.base = uniform(static_cast<const char*>(src) + row0 * stride);
+    m.bytes = n * static_cast<uint32_t>(stride);
+    w.init(first, (kbytes + 127) / 128, steps);
+    w.start(m);
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
       off[q] = ((wave + q * kWaves) * 8 + (lane >> 3)) * static_cast<uint32_t>(stride) + chunk;
@@ -188,13 +218,9 @@ struct KcLoader {
   __device__ __forceinline__ void prepare() {}
   // Load q of the next step (zeros after the last one).
   __device__ __forceinline__ void load(int q, char* lds) {
-    load_to_lds(m, left ? off[q] : kNoOffset, lds + (wave + q * kWaves) * 1024);
+    load_to_lds(m, left > w.pos ? off[q] : kNoOffset, lds + (wave + q * kWaves) * 1024);
   }
-  __device__ __forceinline__ void advance() {
-    m.base += 128;
-    m.bytes = m.bytes > 128 ? m.bytes - 128 : 0;
-    left = left > 128 ? left - 128 : 0;
-  }
+  __device__ __forceinline__ void advance() { w.move(m, w.advance()); }
 };
 
 // KC over the padded vocabulary: a slot of kSlot columns is kSlot rows of one
@@ -206,13 +232,15 @@ struct KcShardLoader {
   uint32_t off[2];
   uint32_t left;
   Span m[NS];
+  RowWalk w;
   int wave;
 
   __device__ __forceinline__ void init(const VocabShards& sh, uint64_t stride, uint32_t col, uint32_t col_end,
-                                       uint32_t kbytes, int wave_, int lane) {
+                                       uint32_t kbytes, uint32_t first, int wave_, int lane) {
     wave = wave_;
     const uint32_t chunk = kc_chunk(wave * 8 + (lane >> 3), lane & 7) * 16;
     left = kbytes > chunk ? kbytes - chunk : 0;
+    w.init(first, (kbytes + 127) / 128, (kbytes + 127) / 128);
 #pragma unroll
     for (int i = 0; i < 2; ++i) off[i] = ((wave + i * kWaves) * 8 + (lane >> 3)) * static_cast<uint32_t>(stride) + chunk;
     int r = 0;
@@ -227,19 +255,17 @@ struct KcShardLoader {
         m[s].base = uniform(static_cast<const char*>(sh.w[r]) + local * stride);
         m[s].bytes = n * static_cast<uint32_t>(stride);
       }
+      w.start(m[s]);
     }
   }
   __device__ __forceinline__ void prepare() {}
   __device__ __forceinline__ void load(int q, char* lds) {
-    load_to_lds(m[q / 2], left ? off[q % 2] : kNoOffset, lds + (wave + q * kWaves) * 1024);
+    load_to_lds(m[q / 2], left > w.pos ? off[q % 2] : kNoOffset, lds + (wave + q * kWaves) * 1024);
   }
   __device__ __forceinline__ void advance() {
+    const int32_t d = w.advance();
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      m[s].base += 128;
-      m[s].bytes = m[s].bytes > 128 ? m[s].bytes - 128 : 0;
-    }
-    left = left > 128 ? left - 128 : 0;
+    for (int s = 0; s < NS; ++s) w.move(m[s], d);
   }
 };
 
@@ -462,6 +488,12 @@ __device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x16_t (&acc
     la.advance();
     lb.advance();
   }
+  // The accumulators end the loop where they were in it (without this the
+  // register allocator moved them about within it for the sake of what follows).
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) asm volatile("" : "+a"(acc[m][n]));
   wait_for_loads();
   __syncthreads();  // the caller may use the LDS
 }
@@ -545,14 +577,21 @@ __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
 
   KcShardLoader<T::BM> la;
   KcLoader<T::BN> lb;
-  la.init(a.sh, a.w_stride, cbase, a.c1, a.kbytes, wave, lane);
-  lb.init(a.x, a.x_stride, t0, a.tokens, a.kbytes, 0, wave, lane);
+  const uint32_t steps = (a.kbytes + 127) / 128;
+  // Tiles of the vocabulary start at different places of their rows: rows are
+  // often a power of two apart, and with every workgroup at the same place the
+  // chip would read from a few memory channels at a time.  Eight tiles share a
+  // start, as they share the tokens' rows in the L2.  (128 x 4096 x 32000, memory
+  // bound: 118 -> 95 us; 8192 x 4096 x 50257: 3.01 -> 2.76 ms.)
+  const uint32_t kfirst = (tm / 8 * 2) % steps;
+  la.init(a.sh, a.w_stride, cbase, a.c1, a.kbytes, kfirst, wave, lane);
+  lb.init(a.x, a.x_stride, t0, a.tokens, a.kbytes, kfirst, steps, wave, lane);
   k_start<T>(lds, la, lb);
   f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
   const int m0 = wm * (T::MT * 32), n0 = wn * (T::NT * 32);
   k_loop<E, T>(
-      lds, (a.kbytes + 127) / 128, acc, la, lb,
+      lds, steps, acc, la, lb,
       [&](const char* t, int m, int s) { return frag_kc<E>(t, m0 + m * 32, s, lane); },
       [&](const char* t, int n, int s) { return frag_kc<E>(t, n0 + n * 32, s, lane); });
 
@@ -724,7 +763,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_hidden_grad(HiddenGradArgs a) {
   KcLoader<T::BN> lb;
   la.init(a.sh, a.w_stride, static_cast<uint64_t>(d0) * esz, static_cast<uint64_t>(a.dim - d0) * esz,
           a.c0 + k_lo * Frag<E>::kBK, a.c0 + k_hi * Frag<E>::kBK, wave, lane);
-  lb.init(a.grad, a.ld * esz, t0, a.grad_rows, (a.c1 - a.c0) * esz, k_lo, wave, lane);
+  lb.init(a.grad, a.ld * esz, t0, a.grad_rows, (a.c1 - a.c0) * esz, k_lo, k_hi - k_lo, wave, lane);
   k_start<T>(lds, la, lb);
   f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
