@@ -484,6 +484,26 @@ def reduce_scatter_dim1(ins, outs, op="sum", stream=None):
     return outs
 
 
+def _on(t):
+    """The context in which a call on t's device launches: the null stream is
+    the current device's."""
+    import contextlib
+
+    import torch
+
+    if t.device.type != "cuda":
+        raise ValueError("buffers must be GPU tensors")
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _given_workspace(workspace, t, what):
+    if not workspace.is_contiguous() or workspace.device != t.device:
+        raise ValueError(f"{what}: the workspace must be contiguous and on the hidden states' device")
+    return workspace
+
+
 def _drop(drop, seed, offset, offset_dev, device):
     import torch
 
@@ -531,7 +551,8 @@ def _dropout_call(func, what, ins, outs, residuals, drop, seed, offset, offset_d
             if q != p or n_res != n_out or z.dtype != y.dtype or z.device != y.device:
                 raise ValueError(f"{what}: residuals must match the outputs in count, length, dtype and device")
         args.insert(1, res)
-    _check(getattr(lib(), func)(*args), func)
+    with _on(x):
+        _check(getattr(lib(), func)(*args), func)
     return ins if outs is None else outs
 
 
@@ -609,6 +630,8 @@ def _vocab_args(hidden, weights, targets, what):
         raise TypeError(f"{what}: targets must be int32 or int64")
     if targets.shape != (hidden.shape[0],) or not targets.is_contiguous() or targets.device != hidden.device:
         raise ValueError(f"{what}: need one contiguous target per token on the hidden states' device")
+    if hidden.device.type != "cuda":
+        raise ValueError(f"{what}: buffers must be GPU tensors")
     return weights, p, vocab
 
 
@@ -639,10 +662,12 @@ def vocab_cross_entropy(hidden, weights, targets, loss=None, lse=None, workspace
     need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 0))
     if workspace is None:
         workspace = _call_workspace(need, hidden, stream)
-    st = lib().rr_vocab_cross_entropy(hidden.data_ptr(), _ptr_array([w.data_ptr() for w in weights]),
-                                      targets.data_ptr(), targets.element_size(), loss.data_ptr(), lse.data_ptr(), p,
-                                      tokens, dim, vocab, code, workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), handle)
+    _given_workspace(workspace, hidden, what)
+    with _on(hidden):
+        st = lib().rr_vocab_cross_entropy(hidden.data_ptr(), _ptr_array([w.data_ptr() for w in weights]),
+                                          targets.data_ptr(), targets.element_size(), loss.data_ptr(), lse.data_ptr(),
+                                          p, tokens, dim, vocab, code, workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), handle)
     _check(st, "rr_vocab_cross_entropy")
     return loss, lse
 
@@ -682,11 +707,13 @@ def vocab_cross_entropy_grad(hidden, weights, targets, lse, grad_loss, dhidden=N
     need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 1))
     if workspace is None:
         workspace = _call_workspace(need, hidden, stream)
-    st = lib().rr_vocab_cross_entropy_grad(
-        hidden.data_ptr(), _ptr_array([w.data_ptr() for w in weights]), targets.data_ptr(), targets.element_size(),
-        lse.data_ptr(), grad_loss.data_ptr(), None if dhidden is None else dhidden.data_ptr(),
-        None if dweights is None else _ptr_array([g.data_ptr() for g in dweights]), p, tokens, dim, vocab, code,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
+    _given_workspace(workspace, hidden, what)
+    with _on(hidden):
+        st = lib().rr_vocab_cross_entropy_grad(
+            hidden.data_ptr(), _ptr_array([w.data_ptr() for w in weights]), targets.data_ptr(), targets.element_size(),
+            lse.data_ptr(), grad_loss.data_ptr(), None if dhidden is None else dhidden.data_ptr(),
+            None if dweights is None else _ptr_array([g.data_ptr() for g in dweights]), p, tokens, dim, vocab, code,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle)
     _check(st, "rr_vocab_cross_entropy_grad")
     return dhidden, dweights
 

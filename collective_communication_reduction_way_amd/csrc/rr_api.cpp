@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -50,6 +51,16 @@ rr_status_t ok() {
 
 rr_status_t hip_fail(hipError_t e, const char* what) {
   return fail(RR_ERROR_HIP, "%s: HIP error %d (%s)", what, static_cast<int>(e), hipGetErrorString(e));
+}
+
+// Runs a call's body; no C++ exception leaves the C boundary.
+template <class F>
+rr_status_t guarded(F f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return RR_ERROR_HIP;  // out of host memory: no message either
+  }
 }
 
 int env_int(const char* name, int dflt) {
@@ -1229,7 +1240,7 @@ static rr_status_t drop_params(rr::DropArgs& a, const rr_dropout_t& d) {
 }
 
 // The four forms: in_len / out_len elements per input / output (and residual) buffer.
-static rr_status_t run_dropout(const char* what, rr::DropForm form, const void* const* send, const void* const* residuals,
+static rr_status_t run_dropout_body(const char* what, rr::DropForm form, const void* const* send, const void* const* residuals,
                         void* const* recv, int p, size_t n, uint64_t in_len, uint64_t out_len, rr_dtype_t dtype,
                         const rr_dropout_t& drop, rr_stream_t stream) {
   rr::DropArgs a;
@@ -1285,6 +1296,14 @@ static rr_status_t run_dropout(const char* what, rr::DropForm form, const void* 
   const hipError_t e = rr::launch_dropout(a, form, kind_of(dtype), reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, what);
   return ok();
+}
+
+static rr_status_t run_dropout(const char* what, rr::DropForm form, const void* const* send,
+                               const void* const* residuals, void* const* recv, int p, size_t n, uint64_t in_len,
+                               uint64_t out_len, rr_dtype_t dtype, const rr_dropout_t& drop, rr_stream_t stream) {
+  return guarded([&] {
+    return run_dropout_body(what, form, send, residuals, recv, p, n, in_len, out_len, dtype, drop, stream);
+  });
 }
 
 static rr_status_t check_shards(int p, size_t n) {
@@ -1466,7 +1485,7 @@ static hipError_t vocab_weight_grad(rr::WeightGradArgs& w, Kind k, rr::VocabTile
   return hipSuccess;
 }
 
-rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weights, const void* targets,
+static rr_status_t vocab_cross_entropy_body(const void* hidden, const void* const* weights, const void* targets,
                                    int target_bytes, float* loss, float* lse, int p, size_t tokens, size_t dim,
                                    size_t vocab, rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
                                    rr_stream_t stream) {
@@ -1542,7 +1561,16 @@ rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weight
   return ok();
 }
 
-rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* weights, const void* targets,
+rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weights, const void* targets,
+                                   int target_bytes, float* loss, float* lse, int p, size_t tokens, size_t dim,
+                                   size_t vocab, rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                   rr_stream_t stream) {
+  return guarded([&] {
+    return vocab_cross_entropy_body(hidden, weights, targets, target_bytes, loss, lse, p, tokens, dim, vocab, dtype, workspace, workspace_bytes, stream);
+  });
+}
+
+static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void* const* weights, const void* targets,
                                         int target_bytes, const float* lse, const float* grad_loss, void* dhidden,
                                         void* const* dweights, int p, size_t tokens, size_t dim, size_t vocab,
                                         rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
@@ -1717,6 +1745,16 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
     if ((e = rr::launch_join(j, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: dhidden");
   }
   return ok();
+}
+
+rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* weights, const void* targets,
+                                        int target_bytes, const float* lse, const float* grad_loss, void* dhidden,
+                                        void* const* dweights, int p, size_t tokens, size_t dim, size_t vocab,
+                                        rr_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                        rr_stream_t stream) {
+  return guarded([&] {
+    return vocab_cross_entropy_grad_body(hidden, weights, targets, target_bytes, lse, grad_loss, dhidden, dweights, p, tokens, dim, vocab, dtype, workspace, workspace_bytes, stream);
+  });
 }
 
 size_t rr_workspace_size(rr_algo_t algo, int p, int group_size, size_t n, rr_dtype_t dtype) {

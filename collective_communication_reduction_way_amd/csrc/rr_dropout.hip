@@ -448,7 +448,12 @@ hipError_t run_dropout(const DropArgs& a, DropForm f, hipStream_t s) {
   const uint64_t windows = ((blocks + kXcds - 1) / kXcds + kGatherW - 1) / kGatherW;
   const uint64_t grid = windows * kGatherW * dst * kXcds;
   const uint64_t written = a.bound[a.chunks] * sizeof(typename E::S) * static_cast<uint64_t>(a.p);
-  if (written > kGatherXcdBytes && grid * kBlock < (1ull << 32)) {
+  // In place a workgroup would drop the shard under the others that still read
+  // it: there one workgroup writes every destination.
+  bool in_place = false;
+  for (int c = 0; c < a.chunks; ++c)
+    in_place = in_place || a.in[c] == static_cast<const char*>(a.out[c]) + a.bound[c] * sizeof(typename E::S);
+  if (written > kGatherXcdBytes && !in_place && grid * kBlock < (1ull << 32)) {
     hipLaunchKernelGGL(k_gather_xcd<E>, dim3(static_cast<uint32_t>(grid)), dim3(kBlock), 0, s, a,
                        static_cast<uint32_t>(per), static_cast<uint32_t>(blocks));
     return hipGetLastError();

@@ -478,7 +478,8 @@ rr_status_t rr_all_gather_dropout(const void* const* sendbufs, void* const* recv
  *     its loss is 0 and nothing depends on it.
  *   loss, lse: float32, [tokens].
  *   workspace: as in rr_all_reduce_ex; rr_vocab_cross_entropy_workspace_size()
- *     bytes.  Its contents mean nothing between calls.
+ *     bytes.  Its contents mean nothing between calls; calls that may overlap
+ *     in time (other streams, graphs replayed together) need one each.
  *   1 <= dim <= 2^20, 1 <= vocab <= 2^23, tokens <= 2^23, tokens*dim and
  *   vocab*dim <= 2^36.  Rows of a multiple of 16 bytes in 16-byte aligned
  *   buffers are read in place; others are copied into aligned rows of the

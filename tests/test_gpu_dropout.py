@@ -208,3 +208,52 @@ def test_long_vector_passes_32_bit_bytes(rr):
                               torch.from_numpy(want).bfloat16().float().numpy()), lo
     del x, out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("in_place", (False, True))
+def test_large_gather_and_in_place(rr, in_place):
+    """Above 128 MiB written a gathered block is read by several workgroups; in
+    place it must be read before it is dropped, once."""
+    p, m = 8, (1 << 20) + 40
+    x = torch.randn(p, m, device="cuda").bfloat16()
+    full = torch.empty(p, p * m, dtype=x.dtype, device="cuda")
+    want = torch.empty(p * m, dtype=x.dtype, device="cuda")
+    rr.dropout([x.reshape(-1)], [want], drop=0.2, seed=3, offset=4)
+    for _ in range(3):
+        full.fill_(float("nan"))
+        src = x
+        if in_place:
+            src = [full[c, c * m:(c + 1) * m] for c in range(p)]
+            for s, d in zip(src, x):
+                s.copy_(d)
+        rr.all_gather_dropout(src, full, drop=0.2, seed=3, offset=4)
+        assert all(torch.equal(full[r], want) for r in range(p))
+
+
+def test_calls_on_two_streams_at_once(rr):
+    x = torch.randn(8, 1 << 20, device="cuda")
+    outs = [torch.empty_like(x) for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        rr.all_reduce_dropout(x, o, drop=0.1, seed=1, offset=i % 2, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3]) and not torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16"))
+@pytest.mark.parametrize("p,n", [(8, 3 * 8 * 65536 + 17), (4, 1 << 21), (12, 700001), (3, 1 << 21)])
+def test_lengths_of_several_workgroups(rr, dtype, p, n):
+    """Vectors long enough for the several-groups-a-lane kernels, compiled and run-time rank counts."""
+    x, res = W.random_inputs(51, p, n, dtype), W.random_inputs(52, p, n, dtype)
+    xs, rs = to_dev(x, dtype), to_dev(res, dtype)
+    out = torch.full_like(xs, float("nan"))
+    rr.all_reduce_dropout(xs, out, drop=0.15, seed=SEED, offset=5, residuals=rs)
+    assert_bitwise(to_host(out, dtype), TR.all_reduce_dropout(x, 0.15, SEED, 5, dtype, res), "all-reduce")
+    rr.dropout(xs, out, drop=0.15, seed=SEED, offset=5, residuals=rs)
+    assert_bitwise(to_host(out, dtype), TR.dropout(x, 0.15, SEED, 5, dtype, res), "ranks")
+    m = n // p
+    xs = xs[:, :m * p].contiguous()
+    sh = torch.full((p, m), float("nan"), dtype=xs.dtype, device="cuda")
+    rr.reduce_scatter_dropout(xs, sh, drop=0.15, seed=SEED, offset=5)
+    assert_bitwise(to_host(sh, dtype), TR.reduce_scatter_dropout(x[:, :m * p], 0.15, SEED, 5, dtype), "reduce-scatter")

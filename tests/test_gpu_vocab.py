@@ -358,3 +358,81 @@ def test_many_tokens_of_one_target(rr):
     check(loss, want[0], tol[0], "loss")
     check(dh, want[2], tol[2], "dhidden")
     check(torch.cat(dw), want[3], tol[3], "dweights")
+
+
+def test_two_streams_at_once(rr):
+    h, w, t, g = inputs(14, 2, 130, 256, 3000, "bfloat16")
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    want = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [rr.vocab_cross_entropy_grad(h, w, t, lse, g, stream=s) for s in streams * 2]
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a, want[0]) and all(torch.equal(x, y) for x, y in zip(b, want[1]))
+
+
+def test_two_graphs_replayed_together(rr):
+    """Each captured call has a workspace of its own, so two graphs may run at the same time."""
+    sides, graphs, outs = [torch.cuda.Stream() for _ in range(2)], [], []
+    data = [inputs(15 + i, 2, 200, 128, 2000, "bfloat16") for i in range(2)]
+    for h, w, t, g in data:
+        loss, lse = rr.vocab_cross_entropy(h, w, t)
+        rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            loss, lse = rr.vocab_cross_entropy(h, w, t)
+            outs.append((loss, *rr.vocab_cross_entropy_grad(h, w, t, lse, g)))
+        graphs.append(graph)
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for s, graph in zip(sides, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (h, w, t, g), (l3, dh3, dw3) in zip(data, outs):
+            loss, lse = rr.vocab_cross_entropy(h, w, t)
+            dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+            assert torch.equal(l3, loss) and torch.equal(dh3, dh) and all(torch.equal(a, b) for a, b in zip(dw3, dw))
+
+
+def test_weights_past_32_bits(rr):
+    """Shards of more than 2^31 elements together and 4 GiB each way: losses and
+    sampled rows of both gradients against float64."""
+    p, T, d, V = 2, 40, 16448, 140001
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    w = torch.empty(V, d, dtype=torch.bfloat16, device="cuda")
+    for lo in range(0, V, 20000):
+        w[lo:lo + 20000].normal_(generator=gen).mul_(1 / d ** 0.5)
+    b = chunk_bounds(V, p)
+    ws = [w[b[r]:b[r + 1]] for r in range(p)]
+    h = torch.randn(T, d, generator=gen, device="cuda").bfloat16()
+    t = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    t[0], t[1], t[2], t[3] = V - 1, 0, b[1], b[1] - 1
+    g = torch.ones(T, device="cuda")
+    loss, lse = rr.vocab_cross_entropy(h, ws, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, ws, t, lse, g)
+    z = torch.cat([h.double() @ w[lo:lo + 20000].double().t() for lo in range(0, V, 20000)], dim=1)
+    wl = torch.logsumexp(z, dim=1)
+    assert ((lse.double() - wl).abs() < 1e-4).all()
+    assert ((loss.double() - (wl - z[torch.arange(T, device="cuda"), t])).abs() < 1e-4).all()
+    z = torch.exp(z - wl[:, None])
+    z[torch.arange(T, device="cuda"), t] -= 1
+    want = sum(z[:, lo:lo + 20000] @ w[lo:lo + 20000].double() for lo in range(0, V, 20000))
+    assert float((dh.double() - want).norm() / want.norm()) < 2 ** -8
+    rows = torch.cat([t, torch.tensor([5, 70000, 131071, 131072, 139999], device="cuda")])
+    got = torch.stack([dw[0][r] if r < b[1] else dw[1][r - b[1]] for r in rows.tolist()]).double()
+    want = z[:, rows].t() @ h.double()
+    assert float((got - want).norm() / want.norm()) < 2 ** -8
+    del w, ws, dw, z
+    torch.cuda.empty_cache()
+
+
+def test_other_workspaces_are_refused(rr):
+    h, w, t, g = inputs(17, 2, 50, 64, 500, "bfloat16")
+    with pytest.raises(rr.RRError):
+        rr.vocab_cross_entropy(h, w, t, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        rr.vocab_cross_entropy(h, w, t, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        rr.vocab_cross_entropy(h.cpu(), [x.cpu() for x in w], t.cpu(), stream=torch.cuda.current_stream())
