@@ -1453,7 +1453,7 @@ static hipError_t vocab_logits(rr::LogitArgs& a, Kind k, rr::VocabTile t, bool g
   const uint32_t cm = rr::tail_start(c0, c1, tiles_over(rows, 256), t);
   char* const g = static_cast<char*>(a.grad);
   for (int tail = 0; tail < 2; ++tail) {
-    const rr::VocabTile tt = tail ? rr::VocabTile::k128x128 : t;
+    const rr::VocabTile tt = tail ? rr::small_tile(k == Kind::kF32) : t;
     a.c0 = tail ? cm : c0;
     a.c1 = tail ? c1 : cm;
     if (a.c0 == a.c1) continue;
@@ -1472,7 +1472,7 @@ static hipError_t vocab_weight_grad(rr::WeightGradArgs& w, Kind k, rr::VocabTile
   const uint32_t cm = rr::tail_start(c0, c1, tiles_over(w.dim, 256), t);
   const char* const g = static_cast<const char*>(w.grad);
   for (int tail = 0; tail < 2; ++tail) {
-    const rr::VocabTile tt = tail ? rr::VocabTile::k128x128 : t;
+    const rr::VocabTile tt = tail ? rr::small_tile(k == Kind::kF32) : t;
     w.c0 = tail ? cm : c0;
     w.c1 = tail ? c1 : cm;
     if (w.c0 == w.c1) continue;
@@ -1742,6 +1742,9 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
     j.tokens = pl.tokens;
     j.dim = pl.dim;
     j.splits = pl.splits;
+    j.vec = reinterpret_cast<uintptr_t>(dhidden) % 8 == 0 && (dim * esz) % 8 == 0 ? 1 : 0;
+    for (int r = 0; r < p; ++r)
+      if (pl.sh.rows[r] && reinterpret_cast<uintptr_t>(weights[r]) % 8) j.vec = 0;
     if ((e = rr::launch_join(j, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: dhidden");
   }
   return ok();

@@ -86,7 +86,7 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
   //     398; 1024 x 4096 x 32000 613 / 587; 512 x 2048 x 16000 133 / 110.
   const uint32_t piece = pl.piece, steps = piece / kSlot;
   const uint64_t tt = ceil_div(tokens, 256), dd = ceil_div(dim, 256), vv = ceil_div(piece, 256);
-  const auto pick = [](bool large) { return large ? VocabTile::k256x256 : VocabTile::k128x128; };
+  const auto pick = [&](bool large) { return large ? VocabTile::k256x256 : small_tile(pl.esz == 4); };
   if (tokens <= 32) {
     pl.logits_tile = pl.hidden_tile = VocabTile::k128x32;
   } else {
@@ -94,13 +94,14 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
     pl.hidden_tile = pick(dd * tt * steps >= 32 * kUnits);
   }
   pl.weight_tile = pick(tokens >= 2048 && dd * vv >= kUnits * 3 / 4);
-  // Few tiles of dhidden: K (the vocabulary) is split over one workgroup a unit,
-  // each with at least 4 steps.  (Two a unit: 256 x 1024 x 16000 62 instead of 55
-  // us, 96 x 768 x 50257 83 instead of 78, 256 x 4096 x 32000 235 instead of 238.)
+  // Few tiles of dhidden: K (the vocabulary) is split over one workgroup a unit
+  // (two of float32's small ones), each with at least 4 steps.  (Two a unit in
+  // bfloat16: 256 x 1024 x 16000 62 instead of 55 us, 96 x 768 x 50257 83 instead of
+  // 78, 256 x 4096 x 32000 235 instead of 238.)
   const uint64_t htiles = static_cast<uint64_t>(ceil_div(dim, tile_m(pl.hidden_tile))) *
                           ceil_div(std::max(tokens, 1u), tile_n(pl.hidden_tile));
-  pl.splits = static_cast<uint32_t>(
-      std::max<uint64_t>(std::min<uint64_t>(kUnits / htiles, std::max(1u, steps / 4)), 1));
+  const uint32_t want = pl.hidden_tile == VocabTile::k128x64 ? 2 * kUnits : kUnits;
+  pl.splits = static_cast<uint32_t>(std::max<uint64_t>(std::min<uint64_t>(want / htiles, std::max(1u, steps / 4)), 1));
 
   for (uint32_t c0 = 0; c0 < off; c0 += pl.piece) {
     const uint32_t c1 = std::min(off, c0 + pl.piece);

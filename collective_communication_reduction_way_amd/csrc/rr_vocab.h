@@ -29,10 +29,11 @@ struct VocabShards {
 };
 
 // Tile of the matrix products: (columns of the M axis) x (columns of the N axis).
-enum class VocabTile : int { k256x256 = 0, k128x128 = 1, k128x32 = 2 };
+// k128x64: float32 only.
+enum class VocabTile : int { k256x256 = 0, k128x128 = 1, k128x32 = 2, k128x64 = 3 };
 constexpr uint32_t tile_m(VocabTile t) { return t == VocabTile::k256x256 ? 256 : 128; }
 constexpr uint32_t tile_n(VocabTile t) {
-  return t == VocabTile::k256x256 ? 256 : t == VocabTile::k128x32 ? 32 : 128;
+  return t == VocabTile::k256x256 ? 256 : t == VocabTile::k128x32 ? 32 : t == VocabTile::k128x64 ? 64 : 128;
 }
 
 // Logits of a piece [c0, c1) of the padded vocabulary.  Forward: the running
@@ -145,6 +146,7 @@ struct JoinArgs {
   const float* lo;        // 16-bit types
   void* out;
   uint32_t tokens, dim, splits;
+  int32_t vec;            // 1: rows of the weights and of dhidden are 8-byte aligned
 };
 
 hipError_t launch_logits(const LogitArgs& a, Kind k, VocabTile t, bool grad, hipStream_t s);
@@ -182,7 +184,10 @@ struct VocabPlan {
   uint64_t part, hit, pack_x, pack_w, xg, grad, acc, tcol, lo, scale, total;
 };
 
-// Where the columns [c0, c1) of a product go over from tiles `t` to 128x128 tiles
+// The tile where there is too little work for the large one.
+constexpr VocabTile small_tile(bool f32) { return f32 ? VocabTile::k128x64 : VocabTile::k128x128; }
+
+// Where the columns [c0, c1) of a product go over from tiles `t` to small tiles
 // (c1: nowhere); other_tiles: the 256-wide tiles of the product's other axis.
 uint32_t tail_start(uint32_t c0, uint32_t c1, uint32_t other_tiles, VocabTile t);
 

@@ -204,6 +204,21 @@ __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
   }
   const HiddenRow<E> h(a.sh, a.tcol, a.lo, a.grad_loss, t, a.tokens, a.dim);
   S* out = static_cast<S*>(a.out) + at;
+  if constexpr (V == 4 && sizeof(S) == 2) {
+    if (a.vec) {
+      if (d >= a.dim) return;
+      h.finish4(v, d, a.dim);
+      uint2 w = make_uint2(0, 0);
+      if (h.live) {
+        if constexpr (__is_same(E, EBF16))
+          w = make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
+        else
+          w = make_uint2(f32x2_to_f16x2_bits(v[0], v[1]), f32x2_to_f16x2_bits(v[2], v[3]));
+      }
+      *reinterpret_cast<uint2*>(out) = w;
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     if (d + j >= a.dim) break;

@@ -18,6 +18,8 @@
 // bytes consecutively.
 #pragma once
 
+#include <type_traits>
+
 #include "rr_device.h"
 #include "rr_vocab_device.h"
 
@@ -383,6 +385,10 @@ struct Tile {
 };
 using T256 = Tile<256, 256, 2, 2>;
 using T128 = Tile<128, 128, 2, 2>;
+// (float32: a compute unit's matrix cores are busy four times as long with the
+// same bytes, so smaller tiles cost nothing and two of them fill each other's
+// waits)
+using T64 = Tile<128, 64, 2, 2>;
 using T32 = Tile<128, 32, 4, 1>;
 
 // The K loop.  A step is 128 bytes of k in four quarters.  While a quarter is
@@ -1029,6 +1035,10 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// small_tile of the kind
+template <class E>
+using Small = std::conditional_t<sizeof(typename E::S) == 4, T64, T128>;
+
 template <class E>
 hipError_t run_logits(const LogitArgs& a, VocabTile t, bool grad, hipStream_t s) {
   const dim3 g(a.tiles_m * a.tiles_n);
@@ -1040,8 +1050,8 @@ hipError_t run_logits(const LogitArgs& a, VocabTile t, bool grad, hipStream_t s)
     hipLaunchKernelGGL((k_logits<E, TT, false>), g, dim3(kWaves * 64), 0, s, a);
   switch (t) {
     case VocabTile::k256x256: RR_LAUNCH(T256) break;
-    case VocabTile::k128x128: RR_LAUNCH(T128) break;
-    default: RR_LAUNCH(T32) break;
+    case VocabTile::k128x32: RR_LAUNCH(T32) break;
+    default: RR_LAUNCH(Small<E>) break;
   }
 #undef RR_LAUNCH
   return hipGetLastError();
@@ -1053,8 +1063,8 @@ hipError_t run_hidden_grad(const HiddenGradArgs& a, VocabTile t, hipStream_t s) 
   if (g.x == 0) return hipSuccess;
   switch (t) {
     case VocabTile::k256x256: hipLaunchKernelGGL((k_hidden_grad<E, T256>), g, dim3(kWaves * 64), 0, s, a); break;
-    case VocabTile::k128x128: hipLaunchKernelGGL((k_hidden_grad<E, T128>), g, dim3(kWaves * 64), 0, s, a); break;
-    default: hipLaunchKernelGGL((k_hidden_grad<E, T32>), g, dim3(kWaves * 64), 0, s, a); break;
+    case VocabTile::k128x32: hipLaunchKernelGGL((k_hidden_grad<E, T32>), g, dim3(kWaves * 64), 0, s, a); break;
+    default: hipLaunchKernelGGL((k_hidden_grad<E, Small<E>>), g, dim3(kWaves * 64), 0, s, a); break;
   }
   return hipGetLastError();
 }
@@ -1066,7 +1076,7 @@ hipError_t run_weight_grad(const WeightGradArgs& a, VocabTile t, hipStream_t s) 
   if (t == VocabTile::k256x256)
     hipLaunchKernelGGL((k_weight_grad<E, T256>), g, dim3(kWaves * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((k_weight_grad<E, T128>), g, dim3(kWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((k_weight_grad<E, Small<E>>), g, dim3(kWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 
