@@ -16,7 +16,8 @@ __device__ __forceinline__ bool counts(const void* targets, int bytes, uint32_t 
 // lse = log sum exp over the tiles' (maximum, sum) pairs and the loss lse -
 // target logit.  P threads share a token, 256 / P tokens a workgroup: 32 where
 // there are many tokens (8 tokens' pairs fill a 64-byte segment), 256 where
-// there are few (one token's few hundred pairs are read at once).
+// there are few (one token's few hundred pairs are read at once: 7.2 -> 3.8 us).
+// 8192 tokens and 197 tiles: 8 us.
 __device__ __forceinline__ void merge(float& mx, float& sum, float m2, float s2) {
   const float top = fmaxf(mx, m2);
   const float ref = top == -__builtin_inff() ? 0.f : top;
@@ -103,6 +104,8 @@ __device__ __forceinline__ void read_chunk(const S* row, uint32_t d, uint32_t di
   }
 }
 
+// A workgroup a row.  Bound by memory: 8192 rows of 4096 bfloat16 values in 23 us
+// (5.8 TB/s).
 template <class E>
 __global__ __launch_bounds__(256) void k_pack_rows(PackRowsArgs a) {
   using S = typename E::S;
