@@ -1,0 +1,120 @@
+"""The training step's ends stay inside their buffers.
+
+Outputs and the caller's workspace lie in one allocation with a sentinel
+before, between and after them, and every byte of it that belongs to no buffer
+must still hold the sentinel after the calls.  The inputs lie between bytes of
+0xFF, NaN in every type, so that a value from past their ends would reach a
+result.  The dropout forms must equal the oracle bit for bit, the cross entropy
+the bits that ordinary buffers gave (test_gpu_vocab checks those against the
+definition)."""
+
+import numpy as np
+import pytest
+
+import workloads as W
+from gpu_util import assert_bitwise, to_dev, to_host
+from oracle import training as TR
+from oracle.collectives import chunk_bounds
+from test_gpu_guard import Guarded
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"float32": torch.float32, "bfloat16": torch.bfloat16, "float16": torch.float16}
+SEED, OFFSET = 0x0123456789ABCDEF, 1 << 40
+
+
+@pytest.fixture(scope="module")
+def rr():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import collective_communication_reduction_way_amd as mod
+
+    mod.lib()
+    return mod
+
+
+def among_nan(t, shift=0):
+    """A copy of `t`, `shift` elements past a 16-byte boundary, with NaN on both sides."""
+    esz = t.element_size()
+    lead = 4096 + shift * esz
+    buf = torch.full((lead + t.numel() * esz + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    v = buf[lead:lead + t.numel() * esz].view(t.dtype).view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("p,m,shift", [(1, 1, 0), (3, 5, 1), (4, 1023, 0), (8, 4097, 3), (8, (1 << 20) + 24, 0), (9, 33, 1)])
+def test_dropout_forms(rr, dtype, p, m, shift):
+    if m > 1 << 20 and dtype != "bfloat16":
+        pytest.skip("one type at the size that takes the other layout of the gather")
+    n, esz = p * m, 4 if dtype == "float32" else 2
+    x = W.random_inputs(31, p, n, dtype)
+    z = W.random_inputs(32, p, n, dtype)
+    xs = [among_nan(to_dev(r, dtype), shift) for r in x]
+    zs = [among_nan(to_dev(r, dtype), shift) for r in z]
+    big = m > 1 << 20
+    runs = [
+        ("gather", n, lambda o: rr.all_gather_dropout([t[:m] for t in xs], o, drop=0.3, seed=SEED, offset=OFFSET),
+         lambda: TR.all_gather_dropout(x[:, :m], 0.3, SEED, OFFSET, dtype)),
+    ]
+    if not big:
+        runs += [
+            ("reduce", n, lambda o: rr.all_reduce_dropout(xs, o, drop=0.3, seed=SEED, offset=OFFSET, residuals=zs),
+             lambda: TR.all_reduce_dropout(x, 0.3, SEED, OFFSET, dtype, z)),
+            ("scatter", m, lambda o: rr.reduce_scatter_dropout(xs, o, drop=0.3, seed=SEED, offset=OFFSET,
+                                                               residuals=[t[:m] for t in zs]),
+             lambda: TR.reduce_scatter_dropout(x, 0.3, SEED, OFFSET, dtype, z[:, :m])),
+            ("ranks", n, lambda o: rr.dropout(xs, o, drop=0.3, seed=SEED, offset=OFFSET, residuals=zs),
+             lambda: TR.dropout(x, 0.3, SEED, OFFSET, dtype, z)),
+        ]
+    for name, length, call, want in runs:
+        g = Guarded([length * esz] * p, dtype, shift * esz)
+        call(g.views())
+        torch.cuda.synchronize()
+        what = f"{name} {dtype} p={p} m={m} shift={shift}"
+        g.check_guards(what)
+        assert_bitwise(np.stack([to_host(v, dtype) for v in g.views()]), want(), what)
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("p,T,d,V,shift", [
+    (1, 1, 8, 1, 0), (1, 1, 1, 9, 0), (3, 7, 72, 130, 0), (8, 33, 256, 1031, 0), (3, 100, 77, 501, 1), (6, 20, 64, 4, 0),
+    (2, 129, 136, 515, 0), (2, 300, 520, 900, 0), (4, 65, 130, 2050, 3),
+    # 256 x 256 tiles, ragged at every end
+    (3, 1025, 264, 9001, 0),
+])
+def test_cross_entropy(rr, dtype, p, T, d, V, shift):
+    gen = torch.Generator().manual_seed(T * 7 + d)
+    h = (torch.randn(T, d, generator=gen) / d ** 0.5).to(DT[dtype]).cuda()
+    b = chunk_bounds(V, p)
+    w = torch.randn(V, d, generator=gen).to(DT[dtype]).cuda()
+    w = [w[b[r]:b[r + 1]].contiguous() for r in range(p)]
+    t = torch.randint(0, V, (T,), generator=gen)
+    t[::5] = -1
+    t = t.cuda()
+    grad = torch.linspace(-1, 1, T).cuda()
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, grad)
+
+    esz = 4 if dtype == "float32" else 2
+    what = f"{dtype} p={p} T={T} d={d} V={V} shift={shift}"
+    h2, w2 = among_nan(h, shift), [among_nan(x, shift) for x in w]
+    t2, grad2 = among_nan(t), among_nan(grad)
+    need = [rr.vocab_cross_entropy_workspace_size(p, T, d, V, DT[dtype], grad=k) for k in (False, True)]
+    g = Guarded([T * 4, T * 4] + need, "float32")
+    loss2, lse2 = g.view(0), g.view(1)
+    ws = [g.buf[o:o + nb] for o, nb in zip(g.offsets[2:], need)]
+    o = Guarded([T * d * esz] + [x.numel() * esz for x in w], dtype, shift * esz)
+    dh2, dw2 = o.view(0, (T, d)), [o.view(1 + r, w[r].shape) for r in range(p)]
+    rr.vocab_cross_entropy(h2, w2, t2, loss=loss2, lse=lse2, workspace=ws[0])
+    rr.vocab_cross_entropy_grad(h2, w2, t2, lse2, grad2, dhidden=dh2, dweights=dw2, workspace=ws[1])
+    torch.cuda.synchronize()
+    g.check_guards(what)
+    o.check_guards(what)
+    # the buffers' places choose how rows are read and written, not the order of any sum (all
+    # of these vocabularies are one piece)
+    assert torch.equal(loss2, loss) and torch.equal(lse2, lse), what
+    assert torch.equal(dh2, dh), what
+    assert all(torch.equal(x, y) for x, y in zip(dw2, dw)), what
