@@ -923,16 +923,41 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
           static_cast<uint64_t>(a.c1 - a.c0 - v0) * esz, a.rows / Frag<E>::kBK, wave, lane);
   k_start<T>(lds, la, lb);
   // What rounding took from the targets' entries (16-bit types): the tokens
-  // whose target lies in this tile's columns are added as further K steps of
-  // 64.  There are few, since the whole vocabulary shares the tokens: they are
-  // looked up while the first loads arrive, and kept one a lane.
+  // whose target lies in this tile's columns are added as further K steps of up
+  // to 64.  There are few, since the whole vocabulary shares the tokens: they are
+  // looked up while the first loads arrive, and up to 64 of them wait in
+  // registers for the end of the loop, one a lane with its column and remainder
+  // (`entry`), and this thread's chunks of their rows (2048 x 4096 x 32000: 549 us,
+  // 545 without the remainders; 605 with all of it looked up at the end).
   const uint32_t first = a.c0 + v0;
-  uint32_t hits = 0, mine = 0;
+  constexpr uint32_t RA = T::BM * esz, RB = T::BN * esz, kThreads = kWaves * 64;
+  constexpr int NA = T::ABYTES / 16 / kThreads, NB = T::BBYTES / 16 / kThreads;
+  uint32_t hits = 0, entry = 0;
+  u32x4 rows[NA];
+  const auto fetch = [&](const uint32_t* list, uint32_t n) __attribute__((always_inline)) {
+    uint32_t t = 0;
+    entry = 0;
+    if (lane < static_cast<int>(n)) {
+      t = list[lane];
+      entry = (a.tcol[t] - first) << 16 | f32_to_half<E>(a.lo[t]);
+    }
+#pragma unroll
+    for (int u = 0; u < NA; ++u) {
+      const uint32_t i = u * kThreads + threadIdx.x, k = i * 16 / RA;
+      const uint32_t c = ks_chunk<E>(k, (i * 16 % RA) / 16) * 16;
+      rows[u] = u32x4{0, 0, 0, 0};
+      if (u * kThreads * 16 / RA < n) {
+        const uint32_t tk = __shfl(t, static_cast<int>(k));
+        if (k < n && c < xg_cols) rows[u] = *reinterpret_cast<const u32x4*>(xg + tk * a.xg_stride + c);
+      }
+    }
+  };
   if constexpr (esz == 2) {
     uint32_t* const list = reinterpret_cast<uint32_t*>(lds + 2 * T::ABYTES);
     for (uint32_t b = 0; b < a.tokens && hits <= 64; b += kScan)
       scan_targets(a.tcol, a.tokens, b, first, T::BN, list, hits);
-    if (lane < hits && hits <= 64) mine = list[lane];
+    hits = __builtin_amdgcn_readfirstlane(hits);
+    fetch(list, hits <= 64 ? hits : 0);
   }
   f32x16_t acc[T::MT][T::NT];
   const int wm = wave / T::WN, wn = wave % T::WN;
@@ -942,28 +967,44 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
       [&](const char* t, int m, int s) { return frag_ks<E, T::BM>(t, m0 + m * 32, s, lane); },
       [&](const char* t, int n, int s) { return frag_ks<E, T::BN>(t, n0 + n * 32, s, lane); });
   if constexpr (esz == 2) {
+    // the tokens at hand, or, where there were too many, all of them again, 64 at a time
     uint32_t* const list = reinterpret_cast<uint32_t*>(lds + T::ABYTES);
-    const auto add = [&](uint32_t n) {
-      // rows of different tokens: the list's row k, this lane's chunk
-      constexpr uint32_t RB = T::BM * esz;
-      for (uint32_t i = threadIdx.x; i < T::ABYTES / 16; i += kWaves * 64) {
-        const uint32_t k = i * 16 / RB;
-        const uint32_t c = ks_chunk<E>(k, (i * 16 % RB) / 16) * 16;
-        u32x4 v{0, 0, 0, 0};
-        if (k < n && c < xg_cols) v = *reinterpret_cast<const u32x4*>(xg + list[k] * a.xg_stride + c);
-        *reinterpret_cast<u32x4*>(lds + i * 16) = v;
+    const bool held = hits <= 64;
+    uint32_t have = 0, b = 0;
+    for (;;) {
+      uint32_t n = hits;
+      if (!held) {
+        while (have < 64 && b < a.tokens) {
+          scan_targets(a.tcol, a.tokens, b, first, T::BN, list, have);
+          b += kScan;
+        }
+        have = __builtin_amdgcn_readfirstlane(have);
+        n = have < 64 ? have : 64;
+        fetch(list, n);
       }
-      for (uint32_t i = threadIdx.x; i < T::BBYTES / 16; i += kWaves * 64)
-        *reinterpret_cast<u32x4*>(lds + T::BOFF + i * 16) = u32x4{0, 0, 0, 0};
-      __syncthreads();
-      if (threadIdx.x < n) {
-        const uint32_t k = threadIdx.x, t = list[k], c = a.tcol[t] - first;
-        const uint32_t at = k * (T::BN * esz) + (((c >> 4) ^ ks_swizzle<E>(k)) << 5) + (c & 15u) * 2;
-        *reinterpret_cast<S*>(lds + T::BOFF + at) = static_cast<S>(f32_to_half<E>(a.lo[t]));
-      }
+      if (n == 0) break;
+      // A: the tokens' rows; B: in row k the remainder of token k in its column
+      const uint32_t quarters = (n + 15) / 16;
+#pragma unroll
+      for (int u = 0; u < NA; ++u)
+        if (u * kThreads * 16 / RA < quarters * 16)
+          *reinterpret_cast<u32x4*>(lds + (u * kThreads + threadIdx.x) * 16) = rows[u];
+#pragma unroll
+      for (int u = 0; u < NB; ++u)
+        if (u * kThreads * 16 / RB < quarters * 16) {
+          const uint32_t i = u * kThreads + threadIdx.x, k = i * 16 / RB;
+          const uint32_t e = __shfl(entry, static_cast<int>(k)), col = e >> 16;
+          const uint32_t w = (e & 0xffffu) << (col % 2 * 16);
+          const bool here = col / 8 == ks_chunk<E>(k, (i * 16 % RB) / 16);
+          u32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = here && col % 8 / 2 == static_cast<uint32_t>(j) ? w : 0u;
+          *reinterpret_cast<u32x4*>(lds + T::BOFF + i * 16) = v;
+        }
       __syncthreads();
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
+        if (static_cast<uint32_t>(s) >= quarters) break;
         Frag<E> fa[T::MT], fb[T::NT];
 #pragma unroll
         for (int m = 0; m < T::MT; ++m) fa[m] = frag_ks<E, T::BM>(lds, m0 + m * 32, s, lane);
@@ -975,22 +1016,10 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
           for (int n2 = 0; n2 < T::NT; ++n2) acc[m][n2] = mma<E>(fa[m], fb[n2], acc[m][n2]);
       }
       __syncthreads();
-    };
-    // the list at hand, or, where it was too long, all of it again, 64 at a time
-    uint32_t have = hits <= 64 ? hits : 0, b = hits <= 64 ? a.tokens : 0;
-    if (wave == 0) list[lane] = mine;
-    __syncthreads();
-    for (;;) {
-      while (have < 64 && b < a.tokens) {
-        scan_targets(a.tcol, a.tokens, b, first, T::BN, list, have);
-        b += kScan;
-      }
-      if (have == 0) break;
-      const uint32_t n = have < 64 ? have : 64;
-      add(n);
+      if (held) break;
       have -= n;
       // the rest moves to the front, a workgroup's width at a time
-      for (uint32_t i = 0; i < have; i += kWaves * 64) {
+      for (uint32_t i = 0; i < have; i += kThreads) {
         const uint32_t k = i + threadIdx.x;
         const uint32_t v = k < have ? list[64 + k] : 0;
         __syncthreads();

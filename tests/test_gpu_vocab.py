@@ -360,6 +360,22 @@ def test_many_tokens_of_one_target(rr):
     check(torch.cat(dw), want[3], tol[3], "dweights")
 
 
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("n", (1, 15, 16, 17, 63, 64, 65, 129))
+def test_targets_in_one_tile(rr, n, dtype):
+    """n tokens whose targets share 40 columns, others spread: the remainders
+    of a tile are taken 16 at a time up to 64, more in rounds."""
+    h, w, t, g = inputs(40 + n, 2, 200, 136, 1500, dtype)
+    t.fill_(-1)
+    t[:n] = torch.arange(n, device="cuda") % 40 + 300
+    t[n:n + 20] = torch.arange(700, 700 + min(20, 200 - n), device="cuda")
+    _, lse = rr.vocab_cross_entropy(h, w, t)
+    dh, dw = rr.vocab_cross_entropy_grad(h, w, t, lse, g)
+    want, tol = bounds(h, w, t, g, dtype)
+    check(dh, want[2], tol[2], "dhidden")
+    check(torch.cat(dw), want[3], tol[3], "dweights")
+
+
 def test_two_streams_at_once(rr):
     h, w, t, g = inputs(14, 2, 130, 256, 3000, "bfloat16")
     loss, lse = rr.vocab_cross_entropy(h, w, t)
