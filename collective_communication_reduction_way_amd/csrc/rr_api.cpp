@@ -1623,7 +1623,9 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
   int32_t* scale = reinterpret_cast<int32_t*>(ws + pl.scale);
   uint32_t* tcol = reinterpret_cast<uint32_t*>(ws + pl.tcol);
   float* lo = reinterpret_cast<float*>(ws + pl.lo);
-  if (f16) {
+  const bool short_step = tokens > 0 && tokens <= rr::kRideTokens && !pack;
+  const bool ride_rows = short_step && pl.logits_tile != rr::VocabTile::k256x256;
+  if (f16 && !ride_rows) {
     e = rr::launch_grad_scale(grad_loss, targets, target_bytes, pl.tokens, pl.sh.vocab, scale, s);
     if (e != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: scale");
   }
@@ -1644,11 +1646,17 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
   c.tokens = pl.tokens;
   c.rows = pl.tokens_pad;
   c.dim = pl.dim;
-  if ((e = rr::launch_pack_rows(c, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: copy");
+  if (!ride_rows && (e = rr::launch_pack_rows(c, k, s)) != hipSuccess)
+    return hip_fail(e, "vocab_cross_entropy_grad: copy");
   rr::LogitArgs a;
   memset(&a, 0, sizeof(a));
   a.x = hidden;
   a.x_stride = a.w_stride = dim * pl.esz;
+  if (ride_rows) {
+    a.riders = pl.tokens_pad / rr::kRiderRows;
+    a.xg = c.out;
+    a.scale = scale;
+  }
   if (pack) {
     a.x = c.out;
     a.x_stride = a.w_stride = row;
@@ -1691,6 +1699,21 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
   h.tcol = tcol;
   h.lo = lo;
   h.grad_loss = grad_loss;
+  rr::JoinArgs j;
+  j.sh = sh;
+  j.acc = h.acc;
+  j.split_stride = h.split_stride;
+  j.grad_loss = f16 ? grad_loss : nullptr;
+  j.tcol = tcol;
+  j.lo = lo;
+  j.out = dhidden;
+  j.tokens = pl.tokens;
+  j.dim = pl.dim;
+  j.splits = pl.splits;
+  j.vec = reinterpret_cast<uintptr_t>(dhidden) % 8 == 0 && (dim * esz) % 8 == 0 ? 1 : 0;
+  for (int r = 0; r < p; ++r)
+    if (pl.sh.rows[r] && reinterpret_cast<uintptr_t>(weights[r]) % 8) j.vec = 0;
+  const bool ride_join = short_step && dhidden && dweights && !direct && pl.weight_tile != rr::VocabTile::k256x256;
   rr::WeightGradArgs w;
   memset(&w, 0, sizeof(w));
   w.xg = ws + pl.xg;
@@ -1717,6 +1740,7 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
     a.grad = ws + pl.grad;
     if ((e = vocab_logits(a, k, pl.logits_tile, true, c0, c1, pl.tokens_pad, s)) != hipSuccess)
       return hip_fail(e, "vocab_cross_entropy_grad: logits");
+    a.riders = 0;
     if (dhidden) {
       h.sh = a.sh;
       h.add = c0 > 0 ? 1 : 0;
@@ -1726,27 +1750,17 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
     if (dweights) {
       w.sh = a.sh;
       w.grad = ws + pl.grad;
+      if (ride_join && c1 == pl.sh.off[p]) {
+        w.join = j;
+        w.join_cols = tiles_over(dim, j.splits >= rr::kJoinMany ? 256 : 1024);
+        w.riders = static_cast<uint32_t>((tokens * w.join_cols + 7) / 8 * 8);  // a multiple of the XCDs
+      }
       if ((e = vocab_weight_grad(w, k, pl.weight_tile, c0, c1, s)) != hipSuccess)
         return hip_fail(e, "vocab_cross_entropy_grad: dweights");
     }
   }
-  if (dhidden && !direct) {
-    rr::JoinArgs j;
-    j.sh = sh;
-    j.acc = h.acc;
-    j.split_stride = h.split_stride;
-    j.grad_loss = f16 ? grad_loss : nullptr;
-    j.tcol = tcol;
-    j.lo = lo;
-    j.out = dhidden;
-    j.tokens = pl.tokens;
-    j.dim = pl.dim;
-    j.splits = pl.splits;
-    j.vec = reinterpret_cast<uintptr_t>(dhidden) % 8 == 0 && (dim * esz) % 8 == 0 ? 1 : 0;
-    for (int r = 0; r < p; ++r)
-      if (pl.sh.rows[r] && reinterpret_cast<uintptr_t>(weights[r]) % 8) j.vec = 0;
-    if ((e = rr::launch_join(j, k, s)) != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: dhidden");
-  }
+  if (dhidden && !direct && !ride_join && (e = rr::launch_join(j, k, s)) != hipSuccess)
+    return hip_fail(e, "vocab_cross_entropy_grad: dhidden");
   return ok();
 }
 

@@ -50,7 +50,7 @@ struct LogitArgs {
   float* part;            // forward: [tile][tokens][2] maximum and sum
   float* hit;             // forward: the target's logit
   void* grad;             // gradient: [tokens rounded up to kSlot][ld] in the storage type
-  const uint32_t* tcol;   // gradient: the targets' padded columns (kMasked: none)
+  uint32_t* tcol;         // gradient: the targets' padded columns (kMasked: none)
   float* lo;              // gradient, 16-bit types: what rounding took from the target's entry
   uint64_t ld;
   uint32_t tokens;
@@ -60,7 +60,14 @@ struct LogitArgs {
   uint32_t tile0;         // first forward tile of this piece in `part`
   uint32_t tiles_m, tiles_n;
   int32_t target_bytes;   // 4 or 8
+  // Gradient, short steps: the first `riders` workgroups copy kRiderRows rows
+  // each into xg (PackRowsArgs with unit = 16) and write tcol and, in float16,
+  // scale, which nothing in this launch reads.
+  uint32_t riders;
+  void* xg;
+  int32_t* scale;
 };
+constexpr uint32_t kRiderRows = 8;
 
 // dhidden += grad * W over a piece: accumulators [split][tokens][dim] float32.
 struct HiddenGradArgs {
@@ -81,6 +88,20 @@ struct HiddenGradArgs {
   const float* grad_loss;
 };
 
+// dhidden from the sums of its splits: 4 threads share a column's where there
+// are kJoinMany or more.
+constexpr uint32_t kJoinMany = 8;
+struct JoinPart {
+  const float* acc;
+  uint64_t split_stride;
+  const float* grad_loss; // float16: for the row's scale; else NULL
+  const uint32_t* tcol;
+  const float* lo;        // 16-bit types
+  void* out;
+  uint32_t tokens, dim, splits;
+  int32_t vec;            // 1: rows of the weights and of dhidden are 8-byte aligned
+};
+
 // dweights of a piece = grad^T * xg (xg: the hidden rows that count).
 struct WeightGradArgs {
   VocabShards sh;
@@ -98,6 +119,10 @@ struct WeightGradArgs {
   uint32_t c0, c1;
   uint32_t tiles_m, tiles_n;
   int32_t vec;            // 1: rows of dweights are 16-byte aligned
+  // Short steps: the first `riders` workgroups join dhidden, `join_cols`
+  // workgroups a row of it (dim a multiple of 4).
+  uint32_t riders, join_cols;
+  JoinPart join;
 };
 
 // Copies rows of `dim` elements into rows of out_stride bytes, zero-filled:
@@ -137,16 +162,8 @@ struct LossArgs {
   int32_t target_bytes;
 };
 
-struct JoinArgs {
+struct JoinArgs : JoinPart {
   VocabShards sh;         // the caller's weights
-  const float* acc;
-  uint64_t split_stride;
-  const float* grad_loss; // float16: for the row's scale; else NULL
-  const uint32_t* tcol;
-  const float* lo;        // 16-bit types
-  void* out;
-  uint32_t tokens, dim, splits;
-  int32_t vec;            // 1: rows of the weights and of dhidden are 8-byte aligned
 };
 
 hipError_t launch_logits(const LogitArgs& a, Kind k, VocabTile t, bool grad, hipStream_t s);
@@ -186,6 +203,10 @@ struct VocabPlan {
 
 // The tile where there is too little work for the large one.
 constexpr VocabTile small_tile(bool f32) { return f32 ? VocabTile::k128x64 : VocabTile::k128x128; }
+
+// Up to so many tokens the small passes of the gradient ride on the products'
+// launches (where those are of small tiles and read their inputs in place).
+constexpr uint32_t kRideTokens = 1024;
 
 // Where the columns [c0, c1) of a product go over from tiles `t` to small tiles
 // (c1: nowhere); other_tiles: the 256-wide tiles of the product's other axis.

@@ -8,11 +8,6 @@ namespace rr {
 
 namespace {
 
-__device__ __forceinline__ bool counts(const void* targets, int bytes, uint32_t i, uint32_t vocab) {
-  const int64_t y = target_at(targets, bytes, i);
-  return y >= 0 && y < static_cast<int64_t>(vocab);
-}
-
 // lse = log sum exp over the tiles' (maximum, sum) pairs and the loss lse -
 // target logit.  P threads share a token, 256 / P tokens a workgroup: 32 where
 // there are many tokens (8 tokens' pairs fill a 64-byte segment), 256 where
@@ -69,39 +64,8 @@ __global__ __launch_bounds__(256) void k_loss(LossArgs a) {
 __global__ __launch_bounds__(1024) void k_grad_scale(const float* g, const void* targets, int target_bytes,
                                                      uint32_t tokens, uint32_t vocab, int32_t* scale) {
   __shared__ int sm[16];
-  int top = -150;  // below every float32 exponent
-  for (uint32_t i = threadIdx.x; i < tokens; i += 1024) {
-    const float v = g[i];
-    if (v != 0.f && fabsf(v) < __builtin_inff() && counts(targets, target_bytes, i, vocab))
-      top = max(top, token_exponent(v));
-  }
-  for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = top;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 16; ++i) top = max(top, sm[i]);
-    *scale = top == -150 ? 0 : top;
-  }
-}
-
-// 16 bytes of a row from element d on, zeros from `dim` on; in loads of `unit`
-// bytes where the row goes on that far.
-template <class S>
-__device__ __forceinline__ void read_chunk(const S* row, uint32_t d, uint32_t dim, uint32_t unit, S* out) {
-  constexpr uint32_t EPC = 16 / sizeof(S);
-  const bool whole = d + EPC <= dim;
-  if (whole && unit == 16) {
-    *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(row + d);
-  } else if (whole && unit == 8) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) reinterpret_cast<uint2*>(out)[j] = reinterpret_cast<const uint2*>(row + d)[j];
-  } else if (whole && unit == 4) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t*>(out)[j] = reinterpret_cast<const uint32_t*>(row + d)[j];
-  } else {
-#pragma unroll
-    for (uint32_t j = 0; j < EPC; ++j) out[j] = d + j < dim ? row[d + j] : S(0);
-  }
+  const int top = top_exponent<1024>(g, targets, target_bytes, tokens, vocab, sm);
+  if (threadIdx.x == 0) *scale = top;
 }
 
 // A workgroup a row.  Bound by memory: 8192 rows of 4096 bfloat16 values in 23 us
@@ -109,7 +73,6 @@ __device__ __forceinline__ void read_chunk(const S* row, uint32_t d, uint32_t di
 template <class E>
 __global__ __launch_bounds__(256) void k_pack_rows(PackRowsArgs a) {
   using S = typename E::S;
-  constexpr uint32_t EPC = 16 / sizeof(S);
   const uint32_t t = blockIdx.x;
   uint32_t col = 0;
   if (t < a.tokens && a.targets) {
@@ -117,31 +80,9 @@ __global__ __launch_bounds__(256) void k_pack_rows(PackRowsArgs a) {
     if (a.tcol && threadIdx.x == 0) a.tcol[t] = col;
   }
   const bool live = t < a.tokens && col != kMasked;
-  float f = 1.f;
-  if (a.grad_loss && live) {
-    const float g = a.grad_loss[t];
-    // a row of g = 0 counts for nothing; one of infinite or NaN g makes the
-    // sums that already at scale 1
-    f = g == 0.f ? 0.f : fabsf(g) < __builtin_inff() ? ldexpf(1.f, token_exponent(g) - a.scale[0]) : 1.f;
-  }
-  const S* row = static_cast<const S*>(a.x) + static_cast<uint64_t>(t) * a.dim;
-  char* out = static_cast<char*>(a.out) + t * a.out_stride;
-  for (uint32_t d = threadIdx.x * EPC; d < a.dim; d += 256 * EPC) {
-    __attribute__((aligned(16))) S v[EPC];
-    if (live) {
-      read_chunk<S>(row, d, a.dim, a.unit, v);
-    } else {
-#pragma unroll
-      for (uint32_t j = 0; j < EPC; ++j) v[j] = S(0);
-    }
-    if constexpr (__is_same(E, EF16)) {
-      if (f != 1.f) {
-#pragma unroll
-        for (uint32_t j = 0; j < EPC; ++j) v[j] = static_cast<S>(f32_to_f16_bits(f16_bits_to_f32(v[j]) * f));
-      }
-    }
-    *reinterpret_cast<u32x4*>(out + d * sizeof(S)) = *reinterpret_cast<const u32x4*>(v);
-  }
+  const float f = a.grad_loss && live ? row_factor(a.grad_loss[t], a.scale[0]) : 1.f;
+  copy_row<E, 256>(static_cast<const S*>(a.x) + static_cast<uint64_t>(t) * a.dim,
+                   static_cast<char*>(a.out) + t * a.out_stride, a.dim, a.unit, threadIdx.x, live, f);
 }
 
 template <class S>
@@ -165,75 +106,15 @@ __global__ __launch_bounds__(256) void k_pack_weight(PackWeightArgs a) {
   }
 }
 
-// dhidden = the sum of the splits' float32 accumulators, finished and rounded
-// once.  A workgroup takes 1024 columns of a row, or 256 where there are many
-// splits: then 4 threads share a column's splits, so that a few tokens' few
-// columns are not one long chain of loads.
 template <class E, int G, int V>
 __global__ __launch_bounds__(256) void k_join(JoinArgs a) {
-  using S = typename E::S;
-  constexpr uint32_t kCols = 256 / G * V;
-  __shared__ float part[G][kCols];
-  const uint32_t t = blockIdx.x;
-  const uint32_t c = threadIdx.x % (256 / G), g = threadIdx.x / (256 / G);
-  const uint32_t d = blockIdx.y * kCols + c * V;
-  const uint64_t at = static_cast<uint64_t>(t) * a.dim + d;
-  float v[V] = {};
-  if (d < a.dim) {
-    const float* p = a.acc + at;
-    const uint32_t lo = a.splits * g / G, hi = a.splits * (g + 1) / G;
-#pragma unroll 8
-    for (uint32_t s = lo; s < hi; ++s) {
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p + s * a.split_stride);
-        v[0] += x.x;
-        v[1] += x.y;
-        v[2] += x.z;
-        v[3] += x.w;
-      } else {
-        v[0] += p[s * a.split_stride];
-      }
-    }
-  }
-  if constexpr (G > 1) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) part[g][c * V + j] = v[j];
-    __syncthreads();
-    if (g > 0) return;
-#pragma unroll
-    for (int q = 1; q < G; ++q)
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] += part[q][c * V + j];
-  }
-  const HiddenRow<E> h(a.sh, a.tcol, a.lo, a.grad_loss, t, a.tokens, a.dim);
-  S* out = static_cast<S*>(a.out) + at;
-  if constexpr (V == 4 && sizeof(S) == 2) {
-    if (a.vec) {
-      if (d >= a.dim) return;
-      h.finish4(v, d, a.dim);
-      uint2 w = make_uint2(0, 0);
-      if (h.live) {
-        if constexpr (__is_same(E, EBF16))
-          w = make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]), f32x2_to_bf16x2_bits(v[2], v[3]));
-        else
-          w = make_uint2(f32x2_to_f16x2_bits(v[0], v[1]), f32x2_to_f16x2_bits(v[2], v[3]));
-      }
-      *reinterpret_cast<uint2*>(out) = w;
-      return;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (d + j >= a.dim) break;
-    float w = 0.f;
-    if constexpr (sizeof(S) == 2) w = h.live ? load_one<E>(h.w + d + j) : 0.f;
-    store_one<E>(out + j, h.live ? h.finish(v[j], w) : 0.f);
-  }
+  __shared__ float part[G > 1 ? 256 * V : 1];
+  join_block<E, G, V>(a.sh, a, blockIdx.x, blockIdx.y, part);
 }
 
 template <class E>
 void run_join(const JoinArgs& a, hipStream_t s) {
-  const bool many = a.splits >= 8, vec = a.dim % 4 == 0;
+  const bool many = a.splits >= kJoinMany, vec = a.dim % 4 == 0;
   const uint32_t cols = (many ? 64 : 256) * (vec ? 4 : 1);
   const dim3 g(a.tokens, (a.dim + cols - 1) / cols);
   if (many && vec) hipLaunchKernelGGL((k_join<E, 4, 4>), g, dim3(256), 0, s, a);

@@ -590,13 +590,43 @@ __device__ __forceinline__ void take16(const char* lds, uint32_t cols, SLOT slot
 // 77 MB of weights at 5 TB/s; 2048 tokens, dim 4096: 743 us with its loss.
 // Gradient: exp(z - lse) g in the storage type; the target's 1 is taken off
 // where the tile holds it.
+//
+// RIDERS The copy of the hidden rows for dweights goes along with it in short steps.
+template <class E>
+__device__ __forceinline__ void ride_rows(const LogitArgs& a, int* sm, int wave, int lane) {
+  using S = typename E::S;
+  int top = 0;
+  if constexpr (__is_same(E, EF16)) {
+    top = top_exponent<kWaves * 64>(a.grad_loss, a.targets, a.target_bytes, a.tokens, a.sh.vocab, sm);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = top;
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < kRiderRows / kWaves; ++i) {
+    const uint32_t t = blockIdx.x * kRiderRows + i * kWaves + wave;
+    if (t >= a.grad_rows) break;
+    const uint32_t col = t < a.tokens ? padded_col(a.sh, target_at(a.targets, a.target_bytes, t)) : kMasked;
+    if (t < a.tokens && lane == 0) a.tcol[t] = col;
+    const bool live = col != kMasked;
+    float f = 1.f;
+    if constexpr (__is_same(E, EF16)) f = live ? row_factor(a.grad_loss[t], top) : 1.f;
+    copy_row<E, 64>(reinterpret_cast<const S*>(static_cast<const char*>(a.x) + t * a.x_stride),
+                    static_cast<char*>(a.xg) + t * a.x_stride, a.kbytes / sizeof(S), 16, lane, live, f);
+  }
+}
+
 template <class E, class T, bool GRAD>
 __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
   __shared__ __attribute__((aligned(128))) char lds[T::LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if constexpr (GRAD && T::BN < 256) {
+    if (blockIdx.x < a.riders) {
+      ride_rows<E>(a, reinterpret_cast<int*>(lds), wave, lane);
+      return;
+    }
+  }
   uint32_t tm, tn;
-  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+  tile_of(blockIdx.x - (GRAD && T::BN < 256 ? a.riders : 0), a.tiles_m, a.tiles_n, tm, tn);
   const uint32_t cbase = a.c0 + tm * T::BM;
   const uint32_t t0 = tn * T::BN;
 
@@ -713,7 +743,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
       uint32_t col = kMasked;
       float lse = 0.f, g = 0.f;
       if (t < a.tokens) {
-        col = a.tcol[t];
+        col = T::BN < 256 && a.riders ? padded_col(a.sh, target_at(a.targets, a.target_bytes, t)) : a.tcol[t];
         lse = a.lse[t];
         g = a.grad_loss[t];
       }
@@ -911,8 +941,18 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
   constexpr int esz = sizeof(S);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if constexpr (T::BN < 256) {
+    if (blockIdx.x < a.riders) {
+      const uint32_t t = blockIdx.x / a.join_cols, by = blockIdx.x % a.join_cols;
+      float* const part = reinterpret_cast<float*>(lds);
+      if (t >= a.tokens) return;
+      if (a.join.splits >= kJoinMany) join_block<E, 4, 4>(a.sh, a.join, t, by, part);
+      else join_block<E, 1, 4>(a.sh, a.join, t, by, part);
+      return;
+    }
+  }
   uint32_t tm, tn;
-  tile_of(blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+  tile_of(blockIdx.x - (T::BN < 256 ? a.riders : 0), a.tiles_m, a.tiles_n, tm, tn);
   const uint32_t d0 = tm * T::BM, v0 = tn * T::BN;
   KsLoader<E, T::BM> la;
   KsLoader<E, T::BN> lb;
@@ -1094,7 +1134,7 @@ using Small = std::conditional_t<sizeof(typename E::S) == 4, T64, T128>;
 
 template <class E>
 hipError_t run_logits(const LogitArgs& a, VocabTile t, bool grad, hipStream_t s) {
-  const dim3 g(a.tiles_m * a.tiles_n);
+  const dim3 g(a.riders + a.tiles_m * a.tiles_n);
   if (g.x == 0) return hipSuccess;
 #define RR_LAUNCH(TT)                                                        \
   if (grad)                                                                  \
@@ -1124,7 +1164,7 @@ hipError_t run_hidden_grad(const HiddenGradArgs& a, VocabTile t, hipStream_t s) 
 
 template <class E>
 hipError_t run_weight_grad(const WeightGradArgs& a, VocabTile t, hipStream_t s) {
-  const dim3 g(a.tiles_m * a.tiles_n);
+  const dim3 g(a.riders + a.tiles_m * a.tiles_n);
   if (g.x == 0) return hipSuccess;
   if (t == VocabTile::k256x256)
     hipLaunchKernelGGL((k_weight_grad<E, T256>), g, dim3(kWaves * 64), 0, s, a);
