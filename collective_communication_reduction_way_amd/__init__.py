@@ -202,10 +202,7 @@ def _check(status, func):
 
 
 def _ptr_array(ptrs):
-    arr = (ctypes.c_void_p * max(1, len(ptrs)))()
-    for i, v in enumerate(ptrs):
-        arr[i] = v
-    return arr
+    return (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
 
 
 def _dtype_name(dtype):
@@ -608,14 +605,17 @@ def _vocab_shards(weights, hidden, what):
     weights = list(weights.unbind(0)) if isinstance(weights, torch.Tensor) and weights.dim() == 3 else list(weights)
     if not weights:
         raise ValueError(f"{what}: no weight shards")
-    dim = hidden.shape[1]
+    dim, dtype, device = hidden.shape[1], hidden.dtype, hidden.get_device()
+    rows = []
     for w in weights:
-        if w.dim() != 2 or w.shape[1] != dim or not w.is_contiguous():
+        shape = w.shape
+        if len(shape) != 2 or shape[1] != dim or not w.is_contiguous():
             raise ValueError(f"{what}: weight shards must be contiguous [V_r, {dim}] matrices")
-        if w.dtype != hidden.dtype or w.device != hidden.device:
+        if w.dtype is not dtype or w.get_device() != device:
             raise ValueError(f"{what}: weight shards and hidden states must share device and dtype")
-    p, vocab = len(weights), sum(w.shape[0] for w in weights)
-    if any(w.shape[0] != (r + 1) * vocab // p - r * vocab // p for r, w in enumerate(weights)):
+        rows.append(shape[0])
+    p, vocab = len(rows), sum(rows)
+    if rows != [(r + 1) * vocab // p - r * vocab // p for r in range(p)]:
         raise ValueError(f"{what}: shard r must hold the rows floor(r V / p) .. floor((r + 1) V / p) of V = {vocab}")
     return weights, p, vocab
 
@@ -659,8 +659,8 @@ def vocab_cross_entropy(hidden, weights, targets, loss=None, lse=None, workspace
     _per_token(loss, hidden, what, "loss")
     _per_token(lse, hidden, what, "lse")
     code = _dtype_code(hidden)
-    need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 0))
     if workspace is None:
+        need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 0))
         workspace = _call_workspace(need, hidden, stream)
     _given_workspace(workspace, hidden, what)
     with _on(hidden):
@@ -698,14 +698,16 @@ def vocab_cross_entropy_grad(hidden, weights, targets, lse, grad_loss, dhidden=N
         if dweights is None:
             dweights = [_call_output(hidden, w.shape, w.dtype, stream) for w in weights]
         dweights = list(dweights)
-        if len(dweights) != p or any(g.shape != w.shape or g.dtype != w.dtype or not g.is_contiguous() or
-                                     g.device != w.device for g, w in zip(dweights, weights)):
+        device = hidden.get_device()
+        if len(dweights) != p or not all(
+                [g.shape == w.shape and g.dtype is hidden.dtype and g.is_contiguous() and g.get_device() == device
+                 for g, w in zip(dweights, weights)]):
             raise ValueError(f"{what}: dweights must match the weight shards")
     else:
         dweights = None
     code = _dtype_code(hidden)
-    need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 1))
     if workspace is None:
+        need = int(lib().rr_vocab_cross_entropy_workspace_size(p, tokens, dim, vocab, code, 1))
         workspace = _call_workspace(need, hidden, stream)
     _given_workspace(workspace, hidden, what)
     with _on(hidden):
