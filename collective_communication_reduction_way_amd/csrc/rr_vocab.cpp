@@ -72,7 +72,14 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
   }
   pl.pieces = ceil_div(off, pl.piece);
 
-  // Tiles.  Up to 32 tokens take the narrow one.  The large tile reads least per
+  // Tiles.  Up to 32 tokens take the narrow one.  Logits of up to 64 tokens, or of
+  // so few 128 x 128 tiles that half of the units would idle, take 64 x 64 ones:
+  // the weights are read by more units at once, and less of a tile is padding
+  // (whole step, 128 x 128 / 64 x 64 tiles, us: 90 x 512 x 11000 (86 tiles) 49.7 / 45.4;
+  // 128 x 4096 x 8000 (63) 142 / 125; 500 x 1024 x 2000 (64) 67.5 / 57.9; 128 x 2048 x
+  // 24000 (188) 135 / 139; 50 x 512 x 120000 192 / 148; 60 x 1024 x 60000 145.1 / 144.6;
+  // float32, 128 x 64 / 64 x 64: 250 x 1024 x 12000 (188) 263 / 236, 60 x 1024 x 60000
+  // (469) 340 / 344).  The large tile reads least per
   // product, but only one workgroup fits on a compute unit, so nothing
   // overlaps its first loads and its output: it needs enough tiles for the
   // units, and enough steps of K in each.  Measured in bfloat16 on cold caches
@@ -90,7 +97,10 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
   if (tokens <= 32) {
     pl.logits_tile = pl.hidden_tile = VocabTile::k128x32;
   } else {
+    const uint64_t tiles = static_cast<uint64_t>(ceil_div(piece, 128)) * ceil_div(tokens, 128);
+    const bool f32 = pl.esz == 4;
     pl.logits_tile = pick(vv * tt >= kUnits);
+    if (f32 ? tiles <= kUnits : tiles <= kUnits / 2 || tokens <= 64) pl.logits_tile = VocabTile::k64x64;
     pl.hidden_tile = pick(dd * tt * steps >= 32 * kUnits);
   }
   pl.weight_tile = pick(tokens >= 2048 && dd * vv >= kUnits * 3 / 4);

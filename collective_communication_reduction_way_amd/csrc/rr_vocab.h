@@ -29,11 +29,18 @@ struct VocabShards {
 };
 
 // Tile of the matrix products: (columns of the M axis) x (columns of the N axis).
-// k128x64: float32 only.
-enum class VocabTile : int { k256x256 = 0, k128x128 = 1, k128x32 = 2, k128x64 = 3 };
-constexpr uint32_t tile_m(VocabTile t) { return t == VocabTile::k256x256 ? 256 : 128; }
+// k128x64: float32 only; k64x64: logits only.
+enum class VocabTile : int { k256x256 = 0, k128x128 = 1, k128x32 = 2, k128x64 = 3, k64x64 = 4 };
+constexpr uint32_t tile_m(VocabTile t) {
+  return t == VocabTile::k256x256 ? 256 : t == VocabTile::k64x64 ? 64 : 128;
+}
 constexpr uint32_t tile_n(VocabTile t) {
-  return t == VocabTile::k256x256 ? 256 : t == VocabTile::k128x32 ? 32 : t == VocabTile::k128x64 ? 64 : 128;
+  switch (t) {
+    case VocabTile::k256x256: return 256;
+    case VocabTile::k128x128: return 128;
+    case VocabTile::k128x32: return 32;
+    default: return 64;
+  }
 }
 
 // Logits of a piece [c0, c1) of the padded vocabulary.  Forward: the running

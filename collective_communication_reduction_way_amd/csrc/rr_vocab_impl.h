@@ -401,6 +401,7 @@ using T128 = Tile<128, 128, 2, 2>;
 // same bytes, so smaller tiles cost nothing and two of them fill each other's
 // waits)
 using T64 = Tile<128, 64, 2, 2>;
+using T64x64 = Tile<64, 64, 2, 2>;
 using T32 = Tile<128, 32, 4, 1>;
 
 // The K loop.  A step is 128 bytes of k in four quarters.  While a quarter is
@@ -1144,6 +1145,7 @@ hipError_t run_logits(const LogitArgs& a, VocabTile t, bool grad, hipStream_t s)
   switch (t) {
     case VocabTile::k256x256: RR_LAUNCH(T256) break;
     case VocabTile::k128x32: RR_LAUNCH(T32) break;
+    case VocabTile::k64x64: RR_LAUNCH(T64x64) break;
     default: RR_LAUNCH(Small<E>) break;
   }
 #undef RR_LAUNCH

@@ -82,7 +82,8 @@ def test_dropout_forms(rr, dtype, p, m, shift):
 @pytest.mark.parametrize("p,T,d,V,shift", [
     (1, 1, 8, 1, 0), (1, 1, 1, 9, 0), (3, 7, 72, 130, 0), (8, 33, 256, 1031, 0), (3, 100, 77, 501, 1), (6, 20, 64, 4, 0),
     (2, 129, 136, 515, 0), (2, 300, 520, 900, 0), (4, 65, 130, 2050, 3),
-    # 256 x 256 tiles, ragged at every end
+    # tiles of 128 x 128, and of 256 x 256, ragged at every end
+    (2, 133, 72, 9001, 0), (3, 290, 40, 12003, 0),
     (3, 1025, 264, 9001, 0),
 ])
 def test_cross_entropy(rr, dtype, p, T, d, V, shift):

@@ -128,6 +128,13 @@ def test_against_the_definition(rr, p, T, d, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("p,T,d,V", [(2, 130, 72, 9001), (3, 290, 40, 12003), (5, 64, 104, 20011)])
+def test_wide_vocabularies(rr, p, T, d, V, dtype):
+    """Enough tiles for the middle size of them, and few tokens with many."""
+    run_and_check(rr, p, T, d, V, dtype)
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
 @pytest.mark.parametrize("p,T,d,V,shift", [(2, 5, 1, 40, 0), (3, 33, 77, 501, 0), (1, 70, 333, 1500, 0), (4, 40, 64, 600, 1),
                                            (2, 100, 130, 700, 3)])
 def test_rows_that_are_not_aligned(rr, p, T, d, V, shift, dtype):
