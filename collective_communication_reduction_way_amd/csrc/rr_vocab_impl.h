@@ -592,7 +592,8 @@ __device__ __forceinline__ void take16(const char* lds, uint32_t cols, SLOT slot
 // Gradient: exp(z - lse) g in the storage type; the target's 1 is taken off
 // where the tile holds it.
 //
-// RIDERS The copy of the hidden rows for dweights goes along with it in short steps.
+// In short steps the gradient's first workgroups copy the hidden rows for dweights,
+// a row a wavefront, instead of a launch of their own (kRideTokens).
 template <class E>
 __device__ __forceinline__ void ride_rows(const LogitArgs& a, int* sm, int wave, int lane) {
   using S = typename E::S;
@@ -943,8 +944,9 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if constexpr (T::BN < 256) {
-    if (blockIdx.x < a.riders) {
-      const uint32_t t = blockIdx.x / a.join_cols, by = blockIdx.x % a.join_cols;
+    const uint32_t i = blockIdx.x - a.rider0;
+    if (i < a.riders) {
+      const uint32_t t = i / a.join_cols, by = i % a.join_cols;
       float* const part = reinterpret_cast<float*>(lds);
       if (t >= a.tokens) return;
       if (a.join.splits >= kJoinMany) join_block<E, 4, 4>(a.sh, a.join, t, by, part);
@@ -953,7 +955,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
     }
   }
   uint32_t tm, tn;
-  tile_of(blockIdx.x - (T::BN < 256 ? a.riders : 0), a.tiles_m, a.tiles_n, tm, tn);
+  tile_of(T::BN < 256 && a.rider0 == 0 ? blockIdx.x - a.riders : blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
   const uint32_t d0 = tm * T::BM, v0 = tn * T::BN;
   KsLoader<E, T::BM> la;
   KsLoader<E, T::BN> lb;
