@@ -969,20 +969,23 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
   // whose target lies in this tile's columns are added as further K steps of up
   // to 64.  There are few, since the whole vocabulary shares the tokens: they are
   // looked up while the first loads arrive, and up to 64 of them wait in
-  // registers for the end of the loop, one a lane with its column and remainder
-  // (`entry`), and this thread's chunks of their rows (2048 x 4096 x 32000: 549 us,
+  // registers for the end of the loop, one a lane with its column and remainder,
+  // and this thread's chunks of their rows (2048 x 4096 x 32000: 549 us,
   // 545 without the remainders; 605 with all of it looked up at the end).
   const uint32_t first = a.c0 + v0;
   constexpr uint32_t RA = T::BM * esz, RB = T::BN * esz, kThreads = kWaves * 64;
   constexpr int NA = T::ABYTES / 16 / kThreads, NB = T::BBYTES / 16 / kThreads;
-  uint32_t hits = 0, entry = 0;
+  uint32_t hits = 0, ecol = 0;
+  float elo = 0.f;
   u32x4 rows[NA];
   const auto fetch = [&](const uint32_t* list, uint32_t n) __attribute__((always_inline)) {
     uint32_t t = 0;
-    entry = 0;
+    ecol = first;
+    elo = 0.f;
     if (lane < static_cast<int>(n)) {
       t = list[lane];
-      entry = (a.tcol[t] - first) << 16 | f32_to_half<E>(a.lo[t]);
+      ecol = a.tcol[t];
+      elo = a.lo[t];
     }
 #pragma unroll
     for (int u = 0; u < NA; ++u) {
@@ -1028,6 +1031,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
       if (n == 0) break;
       // A: the tokens' rows; B: in row k the remainder of token k in its column
       const uint32_t quarters = (n + 15) / 16;
+      const uint32_t entry = (ecol - first) << 16 | f32_to_half<E>(elo);
 #pragma unroll
       for (int u = 0; u < NA; ++u)
         if (u * kThreads * 16 / RA < quarters * 16)
