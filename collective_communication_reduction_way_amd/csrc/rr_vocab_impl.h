@@ -446,6 +446,14 @@ template <class E, class T, class LA, class LB, class FA, class FB>
 __device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x16_t (&acc)[T::MT][T::NT], LA& la, LB& lb, FA fa,
                                        FB fb) {
   constexpr int MT = T::MT, NT = T::NT, kMmas = MT * NT;
+  // Where a wavefront has one product a quarter the quarters have four sums (64 x
+  // 64 tiles: two, which leaves registers for four workgroups a compute unit):
+  // shorter chains of roundings (one token, dim 768: logits off by up to 2e-6 at 12.7
+  // with one sum, 9e-7 with four).
+  constexpr int kMore = kMmas > 1 ? 0 : T::BM == 128 ? 3 : 1;
+  f32x16_t more[kMore ? kMore : 1];
+#pragma unroll
+  for (int i = 0; i < kMore; ++i) more[i] = f32x16_t{};
   constexpr int kFirst = kMmas > 1 ? kMmas / 2 : 1;        // the products that the reads go between
   constexpr int kReads = (MT + NT + kFirst - 1) / kFirst;  // fragments read before each of them
 #pragma unroll
@@ -500,7 +508,9 @@ __device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x16_t (&acc
 #pragma unroll
           for (int q = i * LB::NQ / kMmas; q < (i + 1) * LB::NQ / kMmas; ++q) lb.load(q, bc);
         }
-        acc[i / NT][i % NT] = mma<E>(a[s & 1][i / NT], b[s & 1][i % NT], acc[i / NT][i % NT]);
+        constexpr int kSums = kMore + 1;
+        f32x16_t& sum = s % kSums > 0 ? more[s % kSums > 0 ? s % kSums - 1 : 0] : acc[i / NT][i % NT];
+        sum = mma<E>(a[s & 1][i / NT], b[s & 1][i % NT], sum);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -513,6 +523,15 @@ __device__ __forceinline__ void k_loop(char* lds, uint32_t steps, f32x16_t (&acc
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) asm volatile("" : "+a"(acc[m][n]));
+#pragma unroll
+  for (int i = 0; i < kMore; ++i) asm volatile("" : "+a"(more[i]));
+  if constexpr (kMore > 0) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      acc[0][0][x] += more[0][x];
+      if constexpr (kMore == 3) acc[0][0][x] += more[1][x] + more[2][x];
+    }
+  }
   wait_for_loads();
   __syncthreads();  // the caller may use the LDS
 }
