@@ -135,6 +135,18 @@ def test_wide_vocabularies(rr, p, T, d, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
+@pytest.mark.parametrize("p,T,d,V", [(2, 40, 1032, 8001), (2, 900, 1032, 2003), (1, 20, 2056, 5000)])
+def test_short_steps(rr, p, T, d, V, dtype):
+    """The join of dhidden along with dweights: in front of many tiles and behind
+    few, with few splits and with many; one side alone gives the same bits."""
+    (h, w, t, g), (_, lse, dh, dw) = run_and_check(rr, p, T, d, V, dtype)
+    dh1, none = rr.vocab_cross_entropy_grad(h, w, t, lse, g, need_weights=False)
+    assert none is None and torch.equal(dh1, dh)
+    none, dw1 = rr.vocab_cross_entropy_grad(h, w, t, lse, g, need_hidden=False)
+    assert none is None and all(torch.equal(x, y) for x, y in zip(dw1, dw))
+
+
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16", "float16"))
 @pytest.mark.parametrize("p,T,d,V,shift", [(2, 5, 1, 40, 0), (3, 33, 77, 501, 0), (1, 70, 333, 1500, 0), (4, 40, 64, 600, 1),
                                            (2, 100, 130, 700, 3)])
 def test_rows_that_are_not_aligned(rr, p, T, d, V, shift, dtype):
