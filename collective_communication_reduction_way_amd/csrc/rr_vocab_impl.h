@@ -821,8 +821,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
 // dhidden: M = dim, N = tokens, K = the piece's padded columns, in `splits`
 // parts.  Where that is all of K the result is written, else float32 sums.
 // Few tokens give few tiles and the whole vocabulary as K: split, it is read by
-// the whole chip at once (96 x 768 x 50257 in float16: 43 parts, 27.6 us and 5.2
-// for their join).
+// the whole chip at once (96 x 768 x 50257 in float16: 43 parts, 27.8 us;
+// their join rides on dweights' launch).
 template <class E, class T>
 __global__ __launch_bounds__(kWaves * 64) void k_hidden_grad(HiddenGradArgs a) {
   __shared__ __attribute__((aligned(128))) char lds[T::LDS];
