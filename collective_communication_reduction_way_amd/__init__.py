@@ -250,32 +250,38 @@ def _stream(t, stream):
     return stream.cuda_stream
 
 
-def _call_workspace(nbytes, t, stream):
-    """A device workspace for one call, allocated with torch on the current
-    stream.  When the kernels go to another stream, the tensor is marked as
-    used by that stream, so that torch's caching allocator does not hand the
-    block to new work on the current stream while those kernels still write
-    it (the tensor is freed as soon as the call returns)."""
+def _call_empty(shape, dtype, t, stream):
+    """A tensor on t's device for one call that goes to `stream` (None: the
+    current one), allocated on that stream: its block may have been freed by
+    work that is still queued, and only on the stream of the block's pool does
+    that work come first."""
+    import contextlib
+
     import torch
 
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
-        ws.record_stream(stream)
-    return ws
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device)
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=t.device)
+
+
+def _call_workspace(nbytes, t, stream):
+    """A device workspace for one call, freed as soon as the call returns: the
+    block then goes to later work on the call's stream, behind its kernels."""
+    import torch
+
+    return _call_empty(nbytes, torch.uint8, t, stream)
 
 
 def _call_output(t, shape, dtype, stream):
-    """An output tensor for one call, allocated on the current stream and marked
-    as used by the stream the kernels go to (as _call_workspace)."""
+    """An output tensor for one call.  The caller reads it on the current stream
+    (once the call's stream has been waited for): it is marked as used there,
+    so that its block is not written again before those reads end."""
     import torch
 
-    out = torch.empty(shape, dtype=dtype, device=t.device)
+    out = _call_empty(shape, dtype, t, stream)
     if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=t.device)
-        out.record_stream(stream)
+        out.record_stream(torch.cuda.current_stream(t.device))
     return out
 
 
