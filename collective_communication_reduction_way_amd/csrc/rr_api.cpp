@@ -1625,8 +1625,22 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
   float* lo = reinterpret_cast<float*>(ws + pl.lo);
   const bool short_step = tokens > 0 && tokens <= rr::kRideTokens && !pack;
   const bool ride_rows = short_step && pl.logits_tile != rr::VocabTile::k256x256;
-  if (f16 && !ride_rows) {
-    e = rr::launch_grad_scale(grad_loss, targets, target_bytes, pl.tokens, pl.sh.vocab, scale, s);
+  const uint32_t unit = align_unit({reinterpret_cast<uintptr_t>(hidden)}, dim * esz);
+  int32_t* const row_exp = reinterpret_cast<int32_t*>(ws + pl.row_exp);
+  const bool scaled = f16 && dweights;  // the hidden rows of dweights
+  if (scaled) {
+    rr::RowExponentArgs x;
+    x.x = hidden;
+    x.grad_loss = grad_loss;
+    x.targets = targets;
+    x.out = row_exp;
+    x.unit = unit;
+    x.tokens = pl.tokens;
+    x.dim = pl.dim;
+    x.vocab = pl.sh.vocab;
+    x.target_bytes = target_bytes;
+    e = rr::launch_row_exponent(x, s);
+    if (e == hipSuccess && !ride_rows) e = rr::launch_grad_scale(row_exp, pl.tokens, scale, s);
     if (e != hipSuccess) return hip_fail(e, "vocab_cross_entropy_grad: scale");
   }
   // The hidden rows that count, the others zero: a masked token's row may
@@ -1637,12 +1651,12 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
   c.out = ws + pl.xg;
   c.targets = targets;
   c.target_bytes = target_bytes;
-  c.grad_loss = f16 ? grad_loss : nullptr;
+  c.grad_loss = scaled ? grad_loss : nullptr;
   c.scale = scale;
   c.sh = sh;
   c.tcol = tcol;
   c.out_stride = row;
-  c.unit = align_unit({reinterpret_cast<uintptr_t>(hidden)}, dim * pl.esz);
+  c.unit = unit;
   c.tokens = pl.tokens;
   c.rows = pl.tokens_pad;
   c.dim = pl.dim;
@@ -1655,6 +1669,7 @@ static rr_status_t vocab_cross_entropy_grad_body(const void* hidden, const void*
   if (ride_rows) {
     a.riders = pl.tokens_pad / rr::kRiderRows;
     a.xg = c.out;
+    a.row_exp = scaled ? row_exp : nullptr;
     a.scale = scale;
   }
   if (pack) {

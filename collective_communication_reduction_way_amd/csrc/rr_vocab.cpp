@@ -134,6 +134,7 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
     pl.acc = take(static_cast<uint64_t>(pl.splits) * tokens * dim * 4);
     pl.tcol = take(static_cast<uint64_t>(tokens) * 4);
     pl.lo = take(static_cast<uint64_t>(tokens) * 4);
+    if (dt == RR_FLOAT16) pl.row_exp = take(static_cast<uint64_t>(tokens) * 4);
     pl.scale = take(4);
   }
   if (pack) {

@@ -72,6 +72,7 @@ struct LogitArgs {
   // scale, which nothing in this launch reads.
   uint32_t riders;
   void* xg;
+  const int32_t* row_exp; // float16: of k_row_exponent; NULL: the rows are not scaled
   int32_t* scale;
 };
 constexpr uint32_t kRiderRows = 8;
@@ -117,7 +118,7 @@ struct WeightGradArgs {
   uint64_t ld;
   const void* xg;         // [tokens rounded up to kSlot][xg_stride bytes]
   uint64_t xg_stride;
-  const int32_t* scale;   // float16: the device's exponent of the largest loss gradient
+  const int32_t* scale;   // float16: m of the tokens (token_exponent), on the device
   const uint32_t* tcol;   // as in LogitArgs
   const float* lo;
   uint32_t tokens;
@@ -150,6 +151,18 @@ struct PackRowsArgs {
   int32_t target_bytes;
 };
 
+// float16: every token's e + a (token_exponent), kNoExponent where its row counts
+// for nothing.
+struct RowExponentArgs {
+  const void* x;
+  const float* grad_loss;
+  const void* targets;
+  int32_t* out;
+  uint32_t unit;          // as in PackRowsArgs
+  uint32_t tokens, dim, vocab;
+  int32_t target_bytes;
+};
+
 struct PackWeightArgs {
   VocabShards sh;
   void* out;              // row i = padded column c0 + i
@@ -179,8 +192,8 @@ hipError_t launch_weight_grad(const WeightGradArgs& a, Kind k, VocabTile t, hipS
 hipError_t launch_pack_rows(const PackRowsArgs& a, Kind k, hipStream_t s);
 hipError_t launch_pack_weight(const PackWeightArgs& a, Kind k, hipStream_t s);
 hipError_t launch_loss(const LossArgs& a, hipStream_t s);
-hipError_t launch_grad_scale(const float* grad_loss, const void* targets, int target_bytes, uint32_t tokens,
-                             uint32_t vocab, int32_t* scale, hipStream_t s);
+hipError_t launch_row_exponent(const RowExponentArgs& a, hipStream_t s);
+hipError_t launch_grad_scale(const int32_t* row_exp, uint32_t tokens, int32_t* scale, hipStream_t s);
 hipError_t launch_join(const JoinArgs& a, Kind k, hipStream_t s);
 
 // The matrix-product launchers of one element kind (one translation unit each).
@@ -205,7 +218,7 @@ struct VocabPlan {
   uint32_t splits;
   uint32_t tiles;         // forward M tiles over all pieces
   // workspace offsets in bytes
-  uint64_t part, hit, pack_x, pack_w, xg, grad, acc, tcol, lo, scale, total;
+  uint64_t part, hit, pack_x, pack_w, xg, grad, acc, tcol, lo, row_exp, scale, total;
 };
 
 // The tile where there is too little work for the large one.

@@ -25,9 +25,14 @@ __device__ __forceinline__ uint32_t padded_col(const VocabShards& sh, int64_t y)
 // float16 scaling by powers of two.  The gradient of a token's logits is kept
 // as (p - onehot) * g * 2^(15 - e), e the exponent with |g| < 2^e, so that a row
 // keeps its precision whatever the size of its g and probabilities down to
-// about 2^-29 stay normal numbers; the hidden rows of dweights are scaled by
-// 2^(e - e_max).  Neither scaling rounds (the hidden rows only where they
-// become subnormal: tokens that count 2^-10 of the largest or less).
+// about 2^-29 stay normal numbers.  The hidden rows of dweights then have to be
+// scaled by 2^e and a factor that all tokens share: 2^(e - m + 15), where m is the
+// largest e + a of the tokens that count and |h| < 2^a in a token's row, so that
+// the largest row ends just below 2^15.  What lies below 2^-14 after that, less
+// than 2^-29 of the largest |g| |h|, is rounded to a multiple of 2^-24: off by at most
+// 2^-38 of that largest product, far below the float32 sum of a row that it is
+// part of.  (Scaled by 2^(e - e_max) alone, values of 0.02 lost 11 % at a g of 2^-16
+// of the largest.)
 __device__ __forceinline__ int token_exponent(float g) {
   if (!(fabsf(g) < __builtin_inff()) || g == 0.f) return 0;  // inf, NaN and 0 scale to themselves
   return ilogbf(g) + 1;
@@ -77,28 +82,25 @@ __device__ __forceinline__ bool counts(const void* targets, int bytes, uint32_t 
   return y >= 0 && y < static_cast<int64_t>(vocab);
 }
 
-// The largest exponent of the loss gradients that count, by a workgroup of N
-// threads; 0 where none does.  sm: N / 64 words.
+// m of the tokens' e + a (k_row_exponent), by a workgroup of N threads; 0 where
+// none counts.  sm: N / 64 words.
+constexpr int kNoExponent = -1000;  // below every e + a
 template <int N>
-__device__ __forceinline__ int top_exponent(const float* g, const void* targets, int target_bytes, uint32_t tokens,
-                                            uint32_t vocab, int* sm) {
-  int top = -150;  // below every float32 exponent
-  for (uint32_t i = threadIdx.x; i < tokens; i += N) {
-    const float v = g[i];
-    if (v != 0.f && fabsf(v) < __builtin_inff() && counts(targets, target_bytes, i, vocab))
-      top = max(top, token_exponent(v));
-  }
+__device__ __forceinline__ int top_exponent(const int32_t* row_exp, uint32_t tokens, int* sm) {
+  int top = kNoExponent;
+  for (uint32_t i = threadIdx.x; i < tokens; i += N) top = max(top, row_exp[i]);
   for (int o = 32; o > 0; o >>= 1) top = max(top, __shfl_xor(top, o));
   if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = top;
   __syncthreads();
   for (int i = 0; i < N / 64; ++i) top = max(top, sm[i]);
-  return top == -150 ? 0 : top;
+  return top == kNoExponent ? 0 : top;
 }
 
 // The factor of a hidden row in float16's dweights.  A row of g = 0 counts for
-// nothing; one of infinite or NaN g makes the sums that already at scale 1.
+// nothing; one of infinite or NaN g makes the sums that already at scale 1; one
+// without a finite value other than 0 is not in `top`, and its factor stays finite.
 __device__ __forceinline__ float row_factor(float g, int top) {
-  return g == 0.f ? 0.f : fabsf(g) < __builtin_inff() ? ldexpf(1.f, token_exponent(g) - top) : 1.f;
+  return g == 0.f ? 0.f : fabsf(g) < __builtin_inff() ? ldexpf(1.f, min(token_exponent(g) - top + 15, 100)) : 1.f;
 }
 
 // 16 bytes of a row from element d on, zeros from `dim` on; in loads of `unit`

@@ -618,8 +618,10 @@ __device__ __forceinline__ void ride_rows(const LogitArgs& a, int* sm, int wave,
   using S = typename E::S;
   int top = 0;
   if constexpr (__is_same(E, EF16)) {
-    top = top_exponent<kWaves * 64>(a.grad_loss, a.targets, a.target_bytes, a.tokens, a.sh.vocab, sm);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = top;
+    if (a.row_exp) {
+      top = top_exponent<kWaves * 64>(a.row_exp, a.tokens, sm);
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = top;
+    }
   }
 #pragma unroll
   for (uint32_t i = 0; i < kRiderRows / kWaves; ++i) {
@@ -629,7 +631,7 @@ __device__ __forceinline__ void ride_rows(const LogitArgs& a, int* sm, int wave,
     if (t < a.tokens && lane == 0) a.tcol[t] = col;
     const bool live = col != kMasked;
     float f = 1.f;
-    if constexpr (__is_same(E, EF16)) f = live ? row_factor(a.grad_loss[t], top) : 1.f;
+    if constexpr (__is_same(E, EF16)) f = live && a.row_exp ? row_factor(a.grad_loss[t], top) : 1.f;
     copy_row<E, 64>(reinterpret_cast<const S*>(static_cast<const char*>(a.x) + t * a.x_stride),
                     static_cast<char*>(a.xg) + t * a.x_stride, a.kbytes / sizeof(S), 16, lane, live, f);
   }
@@ -1095,7 +1097,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
     }
   }
   float scale = 1.f;
-  if constexpr (__is_same(E, EF16)) scale = ldexpf(1.f, a.scale[0] - 15);
+  if constexpr (__is_same(E, EF16)) scale = ldexpf(1.f, a.scale[0] - 30);
   // row n of the tile: a vocabulary row of one of the shards
   const auto row_of = [&](uint32_t n) -> S* {
     const uint32_t c = a.c0 + v0 + n;

@@ -504,7 +504,9 @@ rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weight
  * Arithmetic: the logits are computed again; g is rounded once to the storage
  * type (float16: scaled by a power of two per token), except that the target's
  * entry keeps twice the type's digits; the products are summed in float32 and
- * rounded once.  The same inputs give the same bits every time.
+ * rounded once.  float16's dweights also round a product grad_loss[t] *
+ * hidden[t][k] where it is below 2^-29 of the largest one of all tokens, to 2^-38
+ * of that.  The same inputs give the same bits every time.
  */
 rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* weights, const void* targets,
                                         int target_bytes, const float* lse, const float* grad_loss, void* dhidden,
