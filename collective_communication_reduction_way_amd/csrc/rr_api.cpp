@@ -1280,6 +1280,12 @@ static rr_status_t run_dropout_body(const char* what, rr::DropForm form, const v
     st = check_aliasing(outs, res, [](const Range& o, const Range& i) { return o.rank == i.rank && o.lo == i.lo; });
     if (st) return st;
   }
+  if (drop.offset_dev) {
+    // every workgroup reads it, at its own time
+    const Range d = range_of(drop.offset_dev, 8, -1);
+    for (const Range& o : outs)
+      if (overlap(o, d)) return fail(RR_ERROR_INVALID_ARGUMENT, "offset_dev lies in the output of rank %d", o.rank);
+  }
   a.has_res = residuals ? 1 : 0;
   a.one_res = one && p > 1 ? 1 : 0;
   a.p = p;

@@ -410,6 +410,7 @@ rr_status_t rr_reduce_scatter_dim1(const void* const* sendbufs, void* const* rec
  *     added to offset when the kernel runs, or NULL.  A captured graph replays its
  *     arguments unchanged; a counter behind offset_dev that the graph or the
  *     caller advances gives every replay its own mask.
+ *     It may not lie in an output.
  * Arithmetic: the fold of the collective in float32, times the scale (one
  * rounding), plus the widened residual (one rounding), converted once.
  */
