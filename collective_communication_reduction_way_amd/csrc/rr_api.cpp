@@ -19,7 +19,6 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
-#include <new>
 #include <string>
 #include <vector>
 
@@ -34,13 +33,23 @@ using rr::Kind;
 
 thread_local std::string g_last_error;
 
+// Fits into the string itself: nothing is allocated.
+rr_status_t out_of_memory() {
+  g_last_error.assign("out of memory");
+  return RR_ERROR_HIP;
+}
+
 rr_status_t fail(rr_status_t st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
+  try {
+    g_last_error = buf;
+  } catch (...) {
+    out_of_memory();
+  }
   return st;
 }
 
@@ -58,8 +67,8 @@ template <class F>
 rr_status_t guarded(F f) {
   try {
     return f();
-  } catch (const std::bad_alloc&) {
-    return RR_ERROR_HIP;  // out of host memory: no message either
+  } catch (...) {
+    return out_of_memory();  // the bodies throw nothing else
   }
 }
 

@@ -87,7 +87,8 @@
  *  - Errors: return codes only.  All validation happens before the first
  *    launch, so a call that returns RR_ERROR_INVALID_ARGUMENT or
  *    RR_ERROR_UNSUPPORTED has written nothing.  A launch failure returns
- *    RR_ERROR_HIP; asynchronous faults surface on the stream's next sync.
+ *    RR_ERROR_HIP (so does running out of host memory in the dropout and cross
+ *    entropy calls); asynchronous faults surface on the stream's next sync.
  *    rr_last_error() gives a message for the calling thread's last failure.
  *  - n == 0 is a valid no-op (RR_SUCCESS, nothing launched) once p, dtype,
  *    op and the rank arrays are valid.
