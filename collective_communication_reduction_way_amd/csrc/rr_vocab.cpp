@@ -25,14 +25,15 @@ uint32_t ceil_div(uint64_t a, uint64_t b) { return static_cast<uint32_t>((a + b 
 
 // A grid of large tiles, one on each compute unit, runs in rounds.  A last round
 // that fills less than half of the units is given to small tiles, which spread
-// it over all of them.
+// it over all of them: as many whole tile columns as do not fit into the rounds
+// before it, where they hold less than half a round.
 uint32_t tail_start(uint32_t c0, uint32_t c1, uint32_t other_tiles, VocabTile t) {
-  if (t != VocabTile::k256x256) return c1;
+  if (t != VocabTile::k256x256 || other_tiles == 0) return c1;
   const uint64_t tiles = static_cast<uint64_t>(ceil_div(c1 - c0, 256)) * other_tiles;
-  const uint64_t rest = tiles % kUnits;
-  if (tiles < kUnits || rest == 0 || 2 * rest >= kUnits) return c1;
   const uint64_t full = tiles / kUnits * kUnits / other_tiles;  // tiles of this axis in full rounds
-  return std::min<uint64_t>(c1, c0 + full * 256);
+  const uint64_t moved = tiles - full * other_tiles;
+  if (tiles < kUnits || moved == 0 || 2 * moved >= kUnits) return c1;
+  return c0 + static_cast<uint32_t>(full) * 256;
 }
 
 void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vocab, rr_dtype_t dt, bool grad,
