@@ -7,7 +7,8 @@ sum).  The hidden row of token t is kept as float16 times 2^(e_t - m + 15), with
 two, so only values below 2^-14 are rounded, to a multiple of 2^-24: off by at
 most 2^-25, which is g_t h_t off by 2^(m - 40).  The gradient of a logit is kept
 as float16 times 2^(15 - e_t): off by u of itself (the target's entry by u^2) and,
-below 2^-14, by 2^-25 or by itself where that is less.  The sums of the products
+below 2^-14, by 2^-25 (2^-39 of |g|, which is 2^(e_t - 1) at least) or by itself
+where that is less.  The sums of the products
 are off by (T + 4) f of their magnitudes, the result by u of itself and 2^-25.
 """
 
@@ -48,7 +49,7 @@ def definition(h, w, t, g):
     # logits and statistics in float32, as a relative error of the probabilities
     Z = ((d + 2) * F * (np.abs(h) @ np.abs(w).T)).max(axis=1)
     L = Z + 16 * F * (np.log(w.shape[0]) + np.abs(lse) + 4)
-    kept = np.where(hot > 0, U * U, U) * np.abs(G) + np.minimum(np.abs(G), 2.0 ** -40)
+    kept = np.where(hot > 0, U * U, U) * np.abs(G) + np.minimum(np.abs(G), 2.0 ** -39)
     dG = ga * (P * (Z + L + 6 * F)[:, None] + kept)
     m = (exponent(g) + exponent(np.abs(h).max(axis=1))).max()
     dw = (G * g[:, None]).T @ h
