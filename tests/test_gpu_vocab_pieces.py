@@ -55,6 +55,7 @@ def inputs(p, T, d, V, dtype, pieces, shift):
     h[:, -1] = 0
     h = h.to(DT[dtype])
     dead = torch.rand(T, generator=gen, device="cuda") < 0.2
+    dead[0] = False  # one token counts at least
     t[dead] = -1
     g = torch.rand(T, generator=gen, device="cuda") * 3 - 1.5
 
