@@ -568,7 +568,8 @@ def all_reduce_dropout(ins, outs=None, drop=0.1, seed=0, offset=0, residuals=Non
     ``offset`` when the kernel runs (for captured graphs).  ``residuals``: None,
     or one tensor per rank (the same tensor may stand for several).  Gradient
     of the inputs: ``dropout`` of each rank's output gradient with the same
-    (seed, offset), where the ranks hold copies of one loss.
+    (seed, offset), where the ranks hold copies of one loss (no autograd graph
+    is recorded).
     """
     return _dropout_call("rr_all_reduce_dropout", "all_reduce_dropout", ins, outs, residuals, drop, seed, offset,
                          offset_dev, stream)
@@ -653,7 +654,9 @@ def vocab_cross_entropy(hidden, weights, targets, loss=None, lse=None, workspace
     cut over p ranks (``weights``: p shards [V_r, dim]); returns (loss, lse),
     float32, one value per token.  The logits are never kept.  A target
     outside the vocabulary masks its token (loss 0).  ``loss``, ``lse`` and the
-    workspace are allocated with torch when not given.
+    workspace are allocated with torch, on the call's stream, when not given.
+    As with every call of this module no autograd graph is recorded: the
+    gradient is ``vocab_cross_entropy_grad``.
     """
     import torch
 

@@ -87,9 +87,11 @@ void plan_vocab(VocabPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t vo
   // (tokens x dim x vocabulary: large / small tile, us):
   //   logits, by the tiles: 1024 x 4096 x 32000 (500 tiles) 233 / 298; 256 x 4096
   //     x 32000 (125) 128 / 118; 512 x 768 x 50257 (394) 71 / 72;
-  //   dhidden, by the steps over all tiles: 2048 x 768 x 50257 (18840) 416 / 435;
-  //     4096 x 512 x 32000 (16000) 395 / 413; 512 x 768 x 50257 (4710) 174 / 162;
+  //   dhidden, by the steps over all tiles: 2048 x 768 x 50257 (18864) 416 / 435;
+  //     4096 x 512 x 32000 (16000) 395 / 413; 512 x 768 x 50257 (4716) 174 / 162;
   //     1024 x 1024 x 8000 (2000) 102 / 71;
+  //     (from 512 tokens on: the rule does not see how much of a large tile fewer
+  //     tokens leave empty, and was not measured there);
   //   dweights, by the tokens: 2048 x 768 x 50257 422 / 435; 4096 x 512 x 32000 354 /
   //     398; 1024 x 4096 x 32000 613 / 587; 512 x 2048 x 16000 133 / 110.
   const uint32_t piece = pl.piece, steps = piece / kSlot;

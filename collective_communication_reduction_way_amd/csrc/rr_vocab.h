@@ -228,7 +228,8 @@ constexpr VocabTile small_tile(bool f32) { return f32 ? VocabTile::k128x64 : Voc
 // rows with float16's scale, the join of dhidden) ride on the products' launches,
 // where those are of small tiles and read their inputs in place: three launches
 // less, about 4 us each (96 x 768 x 50257 float16 step 123.9 -> 113.5 us, 20 x 256 x
-// 4000 52 -> 44; 1024 x 2048 x 4000 float16 128 -> 119).  Longer ones copy and join
+// 4000 52 -> 44; 1024 x 2048 x 4000 float16 128 -> 119; since then float16 has a
+// launch more for the rows' exponents, 3 us).  Longer ones copy and join
 // so much that they want more workgroups a compute unit than the products' LDS
 // leaves.
 constexpr uint32_t kRideTokens = 1024;

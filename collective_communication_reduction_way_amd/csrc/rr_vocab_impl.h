@@ -18,11 +18,11 @@
 // global-to-LDS load writes its 64 x 16 bytes consecutively.
 //
 // What bounds the products.  The large tile: the matrix cores and the power
-// they take.  8192 tokens, dim 4096, 50257 rows, bfloat16: logits 2.91 ms (1160
-// TFLOP/s), their gradient 2.90, dhidden 2.61 (1290 TFLOP/s), dweights 2.91; the
-// matrix cores are busy 54-69% of the cycles at clocks of 1.6 to 1.95 GHz (2.4
-// without load), and a loop of nothing but the products reaches 1590 TFLOP/s on
-// the same data.  A large library product reaches 1360.  A 256 x 256 tile on 4
+// they take.  8192 tokens, dim 4096, 50257 rows, bfloat16: logits 2.92 ms (1160
+// TFLOP/s), their gradient 2.88, dhidden 2.58 (1310 TFLOP/s), dweights 2.77 in two
+// launches; the matrix cores are busy 56-71% of the cycles at clocks of 1.55 to 1.75
+// GHz (2.4 without load), and a loop of nothing but the products reaches 1590
+// TFLOP/s on the same data.  A large library product reaches 1360.  A 256 x 256 tile on 4
 // wavefronts (128 x 128 each) needs two thirds of the LDS reads of 8 wavefronts
 // of 128 x 64, and 32 x 32 instructions keep its 256 accumulators in place where
 // the compiler moved those of 16 x 16 ones about.  The small tiles: loads, and
@@ -606,8 +606,8 @@ __device__ __forceinline__ void take16(const char* lds, uint32_t cols, SLOT slot
 //
 // Forward: the tile's maximum m and sum s = sum exp(z - m) of every token, which
 // k_loss merges as s = s1 exp(m1 - m) + s2 exp(m2 - m): 8 bytes a token and tile
-// leave the chip instead of the logits.  One token, dim 768, 50257 rows: 15.5 us,
-// 77 MB of weights at 5 TB/s; 2048 tokens, dim 4096: 743 us with its loss.
+// leave the chip instead of the logits.  One token, dim 768, 50257 rows: 17 us,
+// 77 MB of weights at 4.5 TB/s; 2048 tokens, dim 4096: 738 us with its loss.
 // Gradient: exp(z - lse) g in the storage type; the target's 1 is taken off
 // where the tile holds it.
 //
@@ -659,8 +659,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
   // Tiles of the vocabulary start at different places of their rows: rows are
   // often a power of two apart, and with every workgroup at the same place the
   // chip would read from a few memory channels at a time.  Eight tiles share a
-  // start, as they share the tokens' rows in the L2.  (128 x 4096 x 32000, memory
-  // bound: 118 -> 95 us; 8192 x 4096 x 50257: 3.01 -> 2.76 ms.)
+  // start, as they share the tokens' rows in the L2.  (Loss of 128 x 4096 x 32000,
+  // memory bound: 80 us with one start, 70 with these; 8192 x 4096 x 50257: the same.)
   const uint32_t kfirst = (tm / 8 * 2) % steps;
   la.init(a.sh, a.w_stride, cbase, a.c1, a.kbytes, kfirst, wave, lane);
   lb.init(a.x, a.x_stride, t0, a.tokens, a.kbytes, kfirst, steps, wave, lane);
@@ -823,7 +823,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_logits(LogitArgs a) {
 // dhidden: M = dim, N = tokens, K = the piece's padded columns, in `splits`
 // parts.  Where that is all of K the result is written, else float32 sums.
 // Few tokens give few tiles and the whole vocabulary as K: split, it is read by
-// the whole chip at once (96 x 768 x 50257 in float16: 43 parts, 27.8 us;
+// the whole chip at once (96 x 768 x 50257 in float16: 42 parts, 27.6 us;
 // their join rides on dweights' launch).
 template <class E, class T>
 __global__ __launch_bounds__(kWaves * 64) void k_hidden_grad(HiddenGradArgs a) {
@@ -955,7 +955,7 @@ __device__ __forceinline__ void scan_targets(const uint32_t* tcol, uint32_t toke
 
 // ---------------------------------------------------------------------------
 // dweights: M = dim, N = the piece's padded columns, K = tokens.  With few tokens
-// it is a write of the whole matrix (96 x 768 x 50257 in float16: 35.6 us for 77
+// it is a write of the whole matrix (96 x 768 x 50257 in float16: 36 us for 77
 // MB, most of it first loads and outputs of 2364 workgroups).
 template <class E, class T>
 __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
@@ -992,7 +992,10 @@ __global__ __launch_bounds__(kWaves * 64) void k_weight_grad(WeightGradArgs a) {
   // looked up while the first loads arrive, and up to 64 of them wait in
   // registers for the end of the loop, one a lane with its column and remainder,
   // and this thread's chunks of their rows (2048 x 4096 x 32000: 549 us,
-  // 545 without the remainders; 605 with all of it looked up at the end).
+  // 545 without the remainders; 605 with all of it looked up at the end).  Tiles
+  // with more of them, as text's commonest tokens give, look them up at the end
+  // (gradient with targets as 1 / rank: 2048 x 4096 x 32000 1431 -> 1453 us, 8192 x
+  // 4096 x 50257 8.16 -> 8.26 ms).
   const uint32_t first = a.c0 + v0;
   constexpr uint32_t RA = T::BM * esz, RB = T::BN * esz, kThreads = kWaves * 64;
   constexpr int NA = T::ABYTES / 16 / kThreads, NB = T::BBYTES / 16 / kThreads;

@@ -517,9 +517,10 @@ rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* w
                                         rr_stream_t stream);
 
 /* Workspace bytes of rr_vocab_cross_entropy (grad = 0) and
- * rr_vocab_cross_entropy_grad (grad != 0); 0 for invalid arguments.  The
- * gradient keeps one part of the logits' gradient at a time, at most 1 GiB (or
- * 256 columns). */
+ * rr_vocab_cross_entropy_grad (grad != 0); 0 for invalid arguments.  They are
+ * enough for buffers of any alignment and for both gradients.  The gradient
+ * keeps one part of the logits' gradient at a time, at most 1 GiB (or 256
+ * columns). */
 size_t rr_vocab_cross_entropy_workspace_size(int p, size_t tokens, size_t dim, size_t vocab, rr_dtype_t dtype,
                                              int grad);
 
