@@ -260,7 +260,8 @@ def _call_empty(shape, dtype, t, stream):
     import torch
 
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=t.device)
+        # torch takes a handle of 0 for none given, not for the null stream
+        stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
     with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=t.device)
 

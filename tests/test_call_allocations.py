@@ -34,11 +34,14 @@ def streams(monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: FakeTensor(state["current"], shape, dtype))
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: state["current"])
-    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: f"stream {handle}")
+    # (a handle of 0 makes torch take some stream of its own instead of the null stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream",
+                        lambda handle, device=None: f"stream {handle}" if handle else "any stream")
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "null stream")
     return state
 
 
-@pytest.mark.parametrize("stream,pool", [(None, "current"), ("side", "side"), (77, "stream 77"), (0, "stream 0")])
+@pytest.mark.parametrize("stream,pool", [(None, "current"), ("side", "side"), (77, "stream 77"), (0, "null stream")])
 def test_allocations_come_from_the_calls_stream(streams, stream, pool):
     t = torch.zeros(1)
     ws = rr._call_workspace(1 << 20, t, stream)

@@ -18,6 +18,23 @@ def rr():
     return mod
 
 
+def test_handle_of_the_null_stream(rr):
+    """A handle of 0 while another stream is the current one."""
+    p, T, d, V = 2, 300, 128, 2500
+    h = torch.randn(T, d, device="cuda").bfloat16()
+    w = [torch.randn(V // p, d, device="cuda").bfloat16() for _ in range(p)]
+    t = torch.randint(0, V, (T,), device="cuda")
+    loss, lse = rr.vocab_cross_entropy(h, w, t)
+    assert torch.cuda.default_stream().cuda_stream == 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        leave_pending_writes([T * 4, rr.vocab_cross_entropy_workspace_size(p, T, d, V, torch.bfloat16)])
+        loss2, lse2 = rr.vocab_cross_entropy(h, w, t, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(loss2, loss) and torch.equal(lse2, lse)
+
+
 def leave_pending_writes(sizes):
     """Blocks of these sizes, freed while their fills wait behind a bounded spin on the current stream."""
     blocks = [torch.empty(nb, dtype=torch.uint8, device="cuda") for nb in sizes for _ in range(3)]
