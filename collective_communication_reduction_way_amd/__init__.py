@@ -259,6 +259,8 @@ def _call_empty(shape, dtype, t, stream):
 
     import torch
 
+    if t.device.type != "cuda":
+        raise ValueError("buffers must be GPU tensors")
     if isinstance(stream, int):
         # torch takes a handle of 0 for none given, not for the null stream
         stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)

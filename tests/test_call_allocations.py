@@ -4,6 +4,7 @@ from that stream's pool: a block from the current stream's pool may still be
 written by kernels queued there, which nothing orders before the call's."""
 
 import contextlib
+from types import SimpleNamespace
 
 import pytest
 
@@ -43,7 +44,7 @@ def streams(monkeypatch):
 
 @pytest.mark.parametrize("stream,pool", [(None, "current"), ("side", "side"), (77, "stream 77"), (0, "null stream")])
 def test_allocations_come_from_the_calls_stream(streams, stream, pool):
-    t = torch.zeros(1)
+    t = SimpleNamespace(device=torch.device("cuda", 0))
     ws = rr._call_workspace(1 << 20, t, stream)
     assert ws.pool == pool and ws.shape == 1 << 20 and ws.dtype is torch.uint8
     out = rr._call_output(t, (5, 3), torch.float32, stream)
