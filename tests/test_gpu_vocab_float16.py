@@ -111,3 +111,27 @@ def test_rows_without_a_size(rr):
     got = dw.double().cpu().numpy()
     assert np.isfinite(got).all() and (np.abs(got - want) <= tol).all()
     assert (dh[5] == 0).all() and (dh[6] == 0).all()
+
+
+@pytest.mark.parametrize("T", (90, 1100))
+def test_captured_steps_follow_their_inputs(rr, T):
+    """The rows' scales are found again at every replay, as the sizes of hidden
+    states and loss gradients change."""
+    h, w, t, g = (x.cuda() for x in two_kinds(T, 72, 2400, 2.0 ** -6, seed=9))
+    _, lse = rr.vocab_cross_entropy(h, [w], t)
+    rr.vocab_cross_entropy_grad(h, [w], t, lse, g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, lse2 = rr.vocab_cross_entropy(h, [w], t)
+        dh2, (dw2,) = rr.vocab_cross_entropy_grad(h, [w], t, lse2, g)
+    for k in range(4):
+        g.mul_((1.0, 2.0 ** -9, 2.0 ** 12, -1.0)[k])
+        h[:, 2:].mul_((1.0, 8.0, 0.25, 1.0)[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        _, lse = rr.vocab_cross_entropy(h, [w], t)
+        dh, (dw,) = rr.vocab_cross_entropy_grad(h, [w], t, lse, g)
+        assert torch.equal(lse2, lse) and torch.equal(dh2, dh) and torch.equal(dw2, dw), k
+        # (|g h| reaches 1.4 * 2^15 * 4, past the largest float16: the targets' rows may be infinite)
+        assert not torch.isnan(dw).any() and float(dw.abs().max()) > 0
