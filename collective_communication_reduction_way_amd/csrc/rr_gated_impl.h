@@ -73,7 +73,8 @@ struct KsPairLoader {
   static constexpr int NQ = KsOffsets<E, R>::NQ;
   KsOffsets<E, R> o;
   const GatedShards* sh;
-  uint64_t stride, col0;
+  uint64_t stride;
+  uint32_t col0;     // bytes, as `cols`
   Span m;            // the next step's rows, at the tile's first column
   uint64_t gate;     // the run's first row of each weight, at the tile's first column
   uint64_t up;
@@ -83,12 +84,12 @@ struct KsPairLoader {
   int r;
   uint32_t mine;
 
-  __device__ __forceinline__ void init(const GatedShards& sh_, uint64_t stride_, uint64_t col0_, uint64_t cols,
+  __device__ __forceinline__ void init(const GatedShards& sh_, uint64_t stride_, uint32_t col0_, uint64_t cols,
                                        uint32_t c_, uint32_t end_, int wave, int lane) {
     mine = wave * 1024;
     sh = &sh_;
     stride = stride_;
-    col0 = col0_;
+    col0 = __builtin_amdgcn_readfirstlane(col0_);
     c = __builtin_amdgcn_readfirstlane(c_);
     end = __builtin_amdgcn_readfirstlane(end_);
     r = -1;
@@ -96,6 +97,7 @@ struct KsPairLoader {
     rows = 0;
     gate = up = 0;
     m.set(nullptr, 0);
+    fix(m);
     o.init(static_cast<uint32_t>(stride), cols, wave, lane);
   }
   __device__ __forceinline__ void place() {
@@ -106,7 +108,8 @@ struct KsPairLoader {
     m.r[0] = static_cast<uint32_t>(base);
     m.r[1] = static_cast<uint32_t>(base >> 32);
     m.r[2] = __builtin_amdgcn_readfirstlane(
-        n && c < end ? n * static_cast<uint32_t>(stride) - static_cast<uint32_t>(col0) : 0);
+        n && c < end ? n * static_cast<uint32_t>(stride) - col0 : 0);
+    fix(m);
   }
   // Before a step: the shard that holds it.
   __device__ __forceinline__ void prepare() {
@@ -603,7 +606,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_gated_hidden(GatedHiddenArgs a)
   KsPairLoader<E, T::BM> la;
   KcLoader<T::BN> lb;
   // (a part that starts inside a run of 64 columns has read nothing of it yet)
-  la.init(a.sh, a.w_stride, static_cast<uint64_t>(d0) * esz, a.w_stride - static_cast<uint64_t>(d0) * esz,
+  la.init(a.sh, a.w_stride, d0 * esz, a.w_stride - static_cast<uint64_t>(d0) * esz,
           a.c0 + k_lo * Frag<E>::kBK, a.c0 + k_hi * Frag<E>::kBK, wave, lane);
   lb.init(a.grad, a.ld * esz, t0, a.tokens, (a.c1 - a.c0) * esz, k_lo, k_hi - k_lo, wave, lane);
   k_start<T>(lds, la, lb);

@@ -55,6 +55,21 @@ struct Span {
 };
 constexpr uint32_t kNoOffset = 0xFFFFFFF0u;  // past the end of every span
 
+// A load may read a scalar register no sooner than five wait states after a vector
+// instruction wrote it.  The compiler, which may form a descriptor's words in vector
+// registers, sees to that for its own instructions, but not for load_to_lds.  So a
+// changed span is fixed: whatever forms it stands in front of fix() and so of all
+// inline assembly that follows, and between that and a load lie five instructions, or
+// wait_for_spans() (k_start, k_loop).  16-bit times within 0.5 %, float32 steps up to 1 %
+// more (with a wait at every change 0.6 and 2 %).
+__device__ __forceinline__ void fix(Span& m) { asm volatile("" : "+s"(m.r)); }
+template <int N>
+__device__ __forceinline__ void fix(Span (&m)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) fix(m[i]);
+}
+__device__ __forceinline__ void wait_for_spans() { asm volatile("s_nop 4"); }
+
 // LDS addresses are 32-bit numbers here: a generic pointer costs a second word and
 // a comparison with null at every use.
 __device__ __forceinline__ uint32_t lds_at(const char* p) {
@@ -218,6 +233,7 @@ struct RowWalk {
       m[i].move(pos);
       if (steps == 0) m[i].r[2] = 0;
     }
+    fix(m);
     if (any) turn(off);
   }
   // On to the next step.  What few steps need stands behind branches that the compiler
@@ -241,6 +257,7 @@ struct RowWalk {
 #pragma unroll
       for (int i = 0; i < M; ++i) m[i].r[2] = 0;
     }
+    fix(m);
   }
 };
 
@@ -314,6 +331,7 @@ struct KsLoader {
     o.init(static_cast<uint32_t>(stride), cols, wave, lane);
     tail = static_cast<uint32_t>(cols < KsOffsets<E, R>::RB ? cols : KsOffsets<E, R>::RB);
     m.set(src, bytes());
+    fix(m);
   }
   __device__ __forceinline__ void prepare() {}
   __device__ __forceinline__ void load(int q, uint32_t lds) {
@@ -323,6 +341,7 @@ struct KsLoader {
     rows = __builtin_amdgcn_readfirstlane(rows < Frag<E>::kBK ? 0 : rows - Frag<E>::kBK);
     m.move(Frag<E>::kBK * stride);
     m.r[2] = bytes();
+    fix(m);
   }
 };
 
@@ -359,6 +378,7 @@ struct KsShardLoader {
     turn = 0;
     rows = 0;
     m.set(nullptr, 0);
+    fix(m);
     o.init(static_cast<uint32_t>(stride), cols, wave, lane);
   }
   // Before a step: the shard that holds it.
@@ -370,6 +390,7 @@ struct KsShardLoader {
       turn = __builtin_amdgcn_readfirstlane(sh->off[r + 1]);
       rows = __builtin_amdgcn_readfirstlane(sh->rows[r] > local ? sh->rows[r] - local : 0);
       m.set(static_cast<const char*>(sh->w[r]) + local * stride + col0, bytes());
+      fix(m);
     }
   }
   __device__ __forceinline__ void load(int q, uint32_t lds) {
@@ -380,6 +401,7 @@ struct KsShardLoader {
     rows = __builtin_amdgcn_readfirstlane(rows < Frag<E>::kBK ? 0 : rows - Frag<E>::kBK);
     m.move(Frag<E>::kBK * stride);
     m.r[2] = bytes();
+    fix(m);
   }
 };
 
@@ -434,6 +456,7 @@ __device__ __forceinline__ void k_start(const char* mem, LA& la, LB& lb) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     la.prepare();
+    wait_for_spans();
 #pragma unroll
     for (int q = 0; q < LA::NQ; ++q) la.load(q, lds + i * T::ABYTES);
 #pragma unroll
@@ -485,6 +508,8 @@ __device__ __forceinline__ void k_loop(const char* mem, uint32_t steps, f32x16_t
     const uint32_t bc = lds_b + (k & 1) * T::BBYTES, bn = lds_b + (~k & 1) * T::BBYTES;
     slot = slot1;
     la.prepare();
+    // (otherwise a product and the addresses of MT + NT fragments or more stand before the first load)
+    if constexpr (kMmas == 1) wait_for_spans();
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s == 3) {
