@@ -865,14 +865,15 @@ def layer_norm_grad(grad_outs, ins, weight, mean, rstd, grad_ins=None, dweight=N
     return grad_ins, dweight, dbias
 
 
-def gated_linear_workspace_size(p, tokens, dim, ffn, dtype, grad=False):
-    """Bytes of workspace gated_linear (or its gradient) needs."""
+def gated_linear_workspace_size(p, tokens, dim, ffn, dtype, grad=False, kept=False):
+    """Bytes of workspace gated_linear (or its gradient) needs; ``kept``: the
+    gradient is given the products that gated_linear kept."""
     import torch
 
     if isinstance(dtype, torch.dtype):
         dtype = _dtype_name(dtype)
     return int(lib().rr_gated_linear_workspace_size(int(p), int(tokens), int(dim), int(ffn), DTYPES[dtype],
-                                                    1 if grad else 0))
+                                                    (2 if kept else 1) if grad else 0))
 
 
 def _matrix_ptrs(bufs, shapes, dtype, device):
@@ -1004,7 +1005,8 @@ def gated_linear_grad(hidden, gate_weights, up_weights, grad_outs, activation="s
         dgate_weights = dup_weights = dg = du = None
     shape = (g.p, g.tokens, g.dim, g.ffn, _dtype_code(hidden))
     if workspace is None:
-        workspace = _call_workspace(int(lib().rr_gated_linear_workspace_size(*shape, 1)), hidden, stream)
+        form = 1 if pre_gates is None else 2
+        workspace = _call_workspace(int(lib().rr_gated_linear_workspace_size(*shape, form)), hidden, stream)
     _given_workspace(workspace, hidden, what)
     with _on(hidden):
         st = lib().rr_gated_linear_grad(hidden.data_ptr(), g.gates, g.ups, *args, dg, du, ACTIVATIONS[activation],

@@ -252,7 +252,7 @@ rr_status_t gated_inputs(GatedCall& c, const void* hidden, const void* const* ga
   for (int r = 0; r < p; ++r)
     if (c.pl.sh.rows[r]) c.pack = c.pack || !aligned16(gates[r]) || !aligned16(ups[r]);
   if ((st = check_workspace(workspace, workspace_bytes,
-                            rr_gated_linear_workspace_size(p, tokens, dim, ffn, dtype, grad ? 1 : 0))))
+                            rr_gated_linear_workspace_size(p, tokens, dim, ffn, dtype, !grad ? 0 : kept ? 2 : 1))))
     return st;
   if (c.pack) plan(true);
   c.sh = c.pl.sh;
@@ -398,8 +398,8 @@ rr_status_t gated_grad_body(const void* hidden, const void* const* gates, const 
   rr_status_t st;
   GatedCall c;
   std::vector<Range> ins, outs;
-  if ((st = gated_inputs(c, hidden, gates, ups, act, p, tokens, dim, ffn, dtype, true, true, workspace,
-                         workspace_bytes, stream, ins)))
+  if ((st = gated_inputs(c, hidden, gates, ups, act, p, tokens, dim, ffn, dtype, true,
+                         pre_gates != nullptr, workspace, workspace_bytes, stream, ins)))
     return st;
   if ((st = check_pre(pre_gates, pre_ups, pre_dtype, dtype))) return st;
   if (!dgates != !dups)
@@ -491,7 +491,7 @@ rr_status_t gated_grad_body(const void* hidden, const void* const* gates, const 
   memset(&j, 0, sizeof(j));
   bool ride_join = false;
   if (dhidden && tokens > 0) {
-    const bool direct = pl.splits == 1 && pl.piece >= all;
+    const bool direct = pl.direct();
     ride_join = !direct && dgates && pl.weight_tile != rr::GatedTile::k256x256 &&
                 tokens <= (f16 ? rr::kGatedRideTokens : rr::kGatedJoinTokens);
     rr::GatedHiddenArgs h;
@@ -647,7 +647,7 @@ size_t rr_gated_linear_workspace_size(int p, size_t tokens, size_t dim, size_t f
   rr::GatedPlan aligned, packed;
   const auto plan = [&](rr::GatedPlan& pl, bool pack) {
     rr::plan_gated(pl, p, static_cast<uint32_t>(tokens), static_cast<uint32_t>(dim), static_cast<uint32_t>(ffn), dtype,
-                   grad != 0, pack, false);
+                   grad != 0, pack, grad == 2);
   };
   plan(packed, true);
   plan(aligned, false);

@@ -137,8 +137,9 @@ void plan_gated(GatedPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t ff
   } else if (f32) {
     pl.forward_tile = pick(ceil_div(columns, 256) * tt >= kUnits);
   } else {
+    // (the gradient's products again, with dh read, are as wide as those that are kept)
     pl.forward_tile = quickest(columns, tokens, ceil_div(dim, 64),
-                               kept ? GatedUse::kForwardWide : GatedUse::kForward);
+                               kept || grad ? GatedUse::kForwardWide : GatedUse::kForward);
   }
   const uint32_t steps = columns / kFeat;
   // dhidden, by the steps of K over all tiles (256 x 256 / 128 x 128, with the activation's
@@ -189,10 +190,10 @@ void plan_gated(GatedPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t ff
   };
   if (grad) {
     pl.grad = take(tokens * pl.ld * pl.esz);
-    pl.acc = take(static_cast<uint64_t>(pl.splits) * tokens * pl.acc_ld * 4);
+    if (!pl.direct()) pl.acc = take(static_cast<uint64_t>(pl.splits) * tokens * pl.acc_ld * 4);
     if (pl.weight_splits > 1) pl.weight_acc = take(pl.weight_splits * pl.ld * pl.acc_ld * 4);
     if (dt == RR_FLOAT16) {
-      pl.pre = take(tokens * pl.ld * 4);
+      if (!kept) pl.pre = take(tokens * pl.ld * 4);
       pl.xs = take(tokens * row);
       pl.row_max = take(static_cast<uint64_t>(tokens) * 4);
       pl.row_exp = take(static_cast<uint64_t>(tokens) * 4);

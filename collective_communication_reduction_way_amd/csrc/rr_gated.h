@@ -206,10 +206,13 @@ struct GatedPlan {
   uint32_t weight_splits;
   // workspace offsets in bytes
   uint64_t pack_x, pack_w, grad, pre, acc, weight_acc, xs, row_max, row_exp, scale, total;
+
+  // dhidden is one product, written without sums of parts.
+  bool direct() const { return splits == 1 && piece >= sh.off[sh.p]; }
 };
 
 // pack: the inputs are copied into aligned rows first; kept: the forward pass keeps its
-// products (the workspace is the same either way).  The sizes must be valid.
+// products, or the gradient is given them.  The sizes must be valid.
 void plan_gated(GatedPlan& pl, int p, uint32_t tokens, uint32_t dim, uint32_t ffn, rr_dtype_t dt, bool grad, bool pack,
                 bool kept);
 

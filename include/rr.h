@@ -627,8 +627,10 @@ rr_status_t rr_gated_linear_grad(const void* hidden, const void* const* gate_wei
                                  size_t tokens, size_t dim, size_t ffn, rr_dtype_t dtype, void* workspace,
                                  size_t workspace_bytes, rr_stream_t stream);
 
-/* Workspace bytes of rr_gated_linear (grad = 0) and rr_gated_linear_grad (grad !=
- * 0); 0 for invalid arguments.  They are enough for buffers of any alignment. */
+/* Workspace bytes of rr_gated_linear (grad = 0) and of rr_gated_linear_grad, with the
+ * products given (grad = 2) or not (any other value, enough for both; float16 computes them
+ * again into the workspace); 0 for invalid arguments.  They are enough for buffers of any
+ * alignment. */
 size_t rr_gated_linear_workspace_size(int p, size_t tokens, size_t dim, size_t ffn, rr_dtype_t dtype, int grad);
 
 /*
