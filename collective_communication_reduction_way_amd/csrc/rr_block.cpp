@@ -93,6 +93,10 @@ rr_status_t norm_body(const void* const* sendbufs, const void* weight, const voi
   a.total = static_cast<uint32_t>(total);
   a.dim = static_cast<uint32_t>(dim);
   a.eps = static_cast<float>(eps);
+  // A lane's sum is of 32 squares at most; scaled by 2^-14 the row's sum fits float32 where
+  // its mean does.  What that loses, below 2^-112 a lane, is nothing beside an eps of 2^-70.
+  a.fit = eps >= 0x1p-70 ? 0x1p-14f : 1.f;
+  a.back = 1.f / a.fit;
   a.center = center ? 1 : 0;
   if (log_launches()) fprintf(stderr, "[rr] layer_norm: p=%d rows=%zu dim=%zu center=%d\n", p, rows, dim, a.center);
   const hipError_t e = rr::launch_norm(a, kind_of(dtype), reinterpret_cast<hipStream_t>(stream));

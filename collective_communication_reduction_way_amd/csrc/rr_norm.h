@@ -27,6 +27,7 @@ struct NormArgs {
   uint32_t rows, total;
   uint32_t dim;
   float eps;
+  float fit, back;  // a power of two that a lane's sum of squares is scaled with, and 1 / fit
   int32_t center;
 };
 

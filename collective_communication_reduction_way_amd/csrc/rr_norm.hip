@@ -197,9 +197,11 @@ __global__ __launch_bounds__(64 * W * forward_rows(W)) void k_norm(NormArgs a) {
         q[1] = fmaf(v[j], v[j], q[1]);
       }
     }
+    q[1] *= a.fit;
     row_sum<W>(q, sm, turn);
+    q[1] *= inv * a.back;
     const float c = a.center ? q[0] * inv : 0.f;
-    const float var = a.center ? fmaxf(fmaf(-c, c, q[1] * inv), 0.f) : q[1] * inv;
+    const float var = a.center ? fmaxf(fmaf(-c, c, q[1]), 0.f) : q[1];
     const float rstd = 1.f / sqrtf(var + a.eps);
     S* const y = static_cast<S*>(a.out[r]) + at;
 #pragma unroll

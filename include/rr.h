@@ -538,8 +538,9 @@ size_t rr_vocab_cross_entropy_workspace_size(int p, size_t tokens, size_t dim, s
  *   mean, rstd: float32, [p * rows] in the order of the ranks: m and 1 / sqrt(v +
  *     eps) of every row, for the gradient; NULL: not kept.  mean must be NULL where
  *     center == 0.
- *   1 <= dim <= 16384, p * rows < 2^31, 0 <= eps finite.  A row whose squares
- *   leave float32 (values beyond about 1e18) has no norm.
+ *   1 <= dim <= 16384, p * rows < 2^31, 0 <= eps finite.  Squares are summed in float32:
+ *   a row of values beyond about 3e18 has rstd = 0 and xh = 0.  With an eps below 1e-21 the sum of
+ *   a row's squares has to be a float32 number with its digits (values of about 1e-18 to 1e17).
  * Arithmetic: float32 throughout, the variance summed about the mean, one
  * rounding to the storage type.
  */
