@@ -982,7 +982,8 @@ def gated_linear_grad(hidden, gate_weights, up_weights, grad_outs, activation="s
     """Gradients of ``gated_linear`` for the outputs' gradients ``grad_outs`` (p
     matrices [tokens, F_r]); returns (dhidden, dgate_weights, dup_weights).
     ``pre_gates`` and ``pre_ups``: what gated_linear kept for the same inputs, or
-    None: the products are computed again.  A side that is not needed is not
+    None: the products are computed again (to the same bits where hidden states and
+    weights are 16-byte aligned as they were there, or neither).  A side that is not needed is not
     computed and returned as None.
     """
     what = "gated_linear_grad"

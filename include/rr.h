@@ -508,7 +508,8 @@ rr_status_t rr_vocab_cross_entropy(const void* hidden, const void* const* weight
  * entry keeps twice the type's digits; the products are summed in float32 and
  * rounded once.  float16's dweights also round a product grad_loss[t] *
  * hidden[t][k] where it is below 2^-29 of the largest one of all tokens, to 2^-38
- * of that.  The same inputs give the same bits every time.
+ * of that.  The same inputs give the same bits every time, in buffers that are
+ * 16-byte aligned and in others; between the two the order of the sums may differ.
  */
 rr_status_t rr_vocab_cross_entropy_grad(const void* hidden, const void* const* weights, const void* targets,
                                         int target_bytes, const float* lse, const float* grad_loss, void* dhidden,
@@ -611,7 +612,7 @@ rr_status_t rr_gated_linear(const void* hidden, const void* const* gate_weights,
  *   dgate_weights[r] = da_r^T * hidden, dup_weights[r] = du_r^T * hidden.
  *   pre_gates, pre_ups: the products a and u that rr_gated_linear kept, or both
  *     NULL: they are computed again (activation checkpointing), to the bits that
- *     float32 keeps.
+ *     float32 keeps where hidden and the weights lie as in the forward call (below).
  *   dhidden: [tokens, dim], or NULL; dgate_weights and dup_weights: p matrices shaped
  *     as the weights, or both NULL; not all of them NULL.  With tokens == 0 the weights'
  *     gradients are filled with zeros.
@@ -619,7 +620,8 @@ rr_status_t rr_gated_linear(const void* hidden, const void* const* gate_weights,
  * type (float16: scaled by a power of two per token); the products are summed in
  * float32 and rounded once.  float16's weights' gradients also round a product da *
  * hidden[t][k] where it is below 2^-29 of the largest one of all tokens, to 2^-38 of
- * that.  The same inputs give the same bits every time.
+ * that.  The same inputs give the same bits every time, in both directions, in buffers
+ * that are 16-byte aligned and in others; between the two the order of the sums may differ.
  */
 rr_status_t rr_gated_linear_grad(const void* hidden, const void* const* gate_weights, const void* const* up_weights,
                                  const void* const* grad_outs, const void* const* pre_gates,
