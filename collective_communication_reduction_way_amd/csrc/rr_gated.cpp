@@ -28,6 +28,10 @@ uint32_t ceil_div(uint64_t a, uint64_t b) { return static_cast<uint32_t>((a + b 
 // 71 / 75 / 68; 2048 x 4096 x 11008 352 / 341 / 316; with both products kept in float32: 8192 x 1024
 // x 4096 177 / 206 / 212; 8192 x 768 x 2048 78 / 91 / 94; 8192 x 2048 x 4096 288 / 311 / 299; 8192 x 4096
 // x 4096 523 / 523 / 488; 1500 x 1024 x 4096 41 / 39 / 51.  It misses 512 x 4096 x 11008, 116 / 148 / 104.
+// (Weights still in the caches.  From memory 128 x 128 tiles, which read most, lose up to a
+// tenth; over 143 drawn shapes what is chosen then takes 0.5 % more than the quickest, at worst 13 %:
+// 512 x 4096 x 11008, and 8192 x 2048 x 4096 kept, 320 / 302 / 281.  A margin for the larger tiles
+// gains at these and loses elsewhere.)
 uint64_t round_time(uint64_t m, uint64_t n, uint32_t steps, GatedTile t, bool wide) {
   const uint64_t tiles = static_cast<uint64_t>(ceil_div(m, tile_m(t))) * ceil_div(n, tile_n(t));
   switch (t) {

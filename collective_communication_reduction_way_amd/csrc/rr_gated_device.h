@@ -49,6 +49,11 @@ __device__ __forceinline__ float activate(float a, float* df) {
 }
 
 // The products' gradients in float32: a becomes dA = dh U act'(A), u dU = dh act(A).
+// They go to the matrix cores rounded to the storage type, as dh and the weights come: a
+// rounding each, of half a step at most.  The results' errors against 64 bits are then those
+// of two roundings, 0.0023 in bfloat16 and 0.0003 in float16, where rounding the results alone
+// leaves 0.0017 and 0.0002.  To take it back each would have to go as two parts, value and
+// remainder, and the gradients' products, three fifths of a long step's time, twice.
 template <class E, GatedAct ACT>
 __device__ __forceinline__ void gate_grad_one(float dh, float& a, float& u) {
   float df;

@@ -61,8 +61,9 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* sm, uint32_t& turn
 // lane keep many rows in flight and few registers in use: rows of 4096 bfloat16
 // values, 8 x 2048 of them, forward with one wavefront a row and 8 chunks a lane
 // 82 us, with four and 2 chunks 45 (5.9 TB/s; a copy of this library 6.4);
-// gradient 122 and, with eight and one chunk, 89 us (6.0 TB/s); 16384 rows of 1024, with one
-// wavefront and 2 chunks 31 us, with two and one chunk 28.
+// gradient with residuals 122 and, with eight and one chunk, 87 us (6.2 TB/s; without
+// residuals 70); 16384 rows of 1024, with one wavefront and 2 chunks 31 us, with two and one
+// chunk 28.
 struct Shape {
   int w, k;
 };
@@ -70,16 +71,16 @@ constexpr int kGradWaves = 8;  // of a workgroup of the gradient: 8 / W rows at 
 constexpr int forward_rows(int W) { return W == 1 ? 4 : 1; }
 
 // Nontemporal stores: what is written is not read here again (rows of 768, 8192 of
-// them: 7.6 -> 6.4 us); nontemporal loads gain in the gradient only (W = 8: 95 -> 89
-// us), where three streams are read.
+// them: 7.6 -> 6.4 us); nontemporal loads gain in the gradient only (W = 8, with
+// residuals: 95 -> 89 us), where three streams are read.
 //
 // A row's last chunk.  No load is conditional: what a branch may skip the compiler has
 // to wait for at once.  A lane whose chunk does not lie in the row whole reads the row's
 // last 16 bytes, and what it reads twice is shifted out where the chunk is used (gradient
 // with residuals, matrices of the size of 15000 x 4096, TB/s, with branches / so: 3000 bfloat16
 // values 2.9 / 4.0, 4095 1.9 / 3.7, 4438 1.4 / 3.3, 1023 float32 ones 3.6 / 5.0).  Rows of less
-// than 16 bytes are read by elements, and 8 chunks a lane, which have no registers to spare, with
-// branches (BRANCH).
+// than 16 bytes are read by elements, and the gradient's 8 chunks a lane, which have no registers
+// to spare, with branches (BRANCH).
 template <class E, bool BRANCH>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t e, uint32_t dim) {  // bytes into the row, or the element (BRANCH)
   if constexpr (BRANCH) return e;
@@ -383,7 +384,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_norm_grad(NormGradArgs a) {
 }
 
 // dweight and dbias: 16 columns a workgroup, 64 threads share four columns' parts, so
-// that 512 parts are one round of loads (512 parts of 4096 columns, both sums: 7.5 us).
+// that 512 parts are one round of loads (512 parts of 4096 columns, both sums: 5 us).
 template <class E>
 __global__ __launch_bounds__(256) void k_norm_join(NormJoinArgs a) {
   using S = typename E::S;
@@ -438,8 +439,8 @@ Shape grad_shape(uint32_t dim, Kind k) {
 constexpr uint32_t kNormGrid = 1u << 20;  // workgroups of the forward pass at most
 // Of the gradient, two a compute unit where their lines of sums are little beside the
 // rows (a tenth; both go with the row's length, so that the rows decide), else one, and
-// rows evenly over them.  With the join, 512 / 256 workgroups, us: bfloat16, 16384 rows of
-// 4096 79 / 83 (1024: 87), 4096 rows 33 / 32, 2048 rows 26 / 23, 300 rows 15 with 256 and 12
+// rows evenly over them.  Without residuals, with the join, 512 / 256 workgroups, us: bfloat16,
+// 16384 rows of 4096 79 / 83 (1024: 87), 4096 rows 33 / 32, 2048 rows 26 / 23, 300 rows 15 with 256 and 12
 // with 150; 2000 rows of 2048 16.2 / 13.8; 4096 rows of 1024 12.7 / 11.4; 8192 rows of 768
 // 17.3 / 20.0; 999 float32 rows of 1023 11.8 / 10.3, 4096 of 768 15.0 / 16.0.
 constexpr uint32_t kNormGradGrid = 512;
